@@ -36,6 +36,10 @@ PATH_AUTO = 0
 PATH_SIMT = 1
 PATH_TC = 2
 
+ACT_NONE = 0
+ACT_SILU = 1
+ACT_GELU = 2
+
 _vp, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
 _SIGS = {
@@ -70,6 +74,21 @@ _SIGS = {
     "eqlin_d8_fourier_mlp_workspace_bytes": (_sz, [_i64, _i, _i, _i]),
     "eqlin_d8_fourier_mlp_ws": (_i, [_vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _vp, _sz, _vp]),
     "eqlin_d8_fourier_mlp": (_i, [_vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _vp]),
+    "eqlin_cyclic_gated_spectrum_bytes": (_sz, [_i, _i, _i, _i]),
+    "eqlin_cyclic_gated_weight_spectrum": (_i, [_vp, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "eqlin_cyclic_gated_adjoint_bytes": (_sz, [_i, _i, _i, _i]),
+    "eqlin_cyclic_gated_weight_spectrum_adjoint": (_i, [_vp, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "eqlin_cyclic_gated_auto_path": (_i, [_i, _i, _i, _i]),
+    "eqlin_cyclic_gated_forward": (_i, [_vp, _vp, _vp, _i64, _i, _i, _i, _i, _i, _i, _vp]),
+    "eqlin_cyclic_gated_backward_workspace_bytes": (_sz, [_i64, _i, _i, _i, _i]),
+    "eqlin_cyclic_gated_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _i, _i, _vp, _sz,
+                                         _vp]),
+    "eqlin_group_norm_workspace_bytes": (_sz, [_i64, _i64, _i, _i, _i, _i]),
+    "eqlin_group_norm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i, _i, _i, ctypes.c_float, _i, _i, _vp,
+                              _sz, _vp]),
+    "eqlin_group_norm_backward_workspace_bytes": (_sz, [_i64, _i64, _i, _i, _i, _i]),
+    "eqlin_group_norm_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i, _i, _i, _i,
+                                       _i, _vp, _sz, _vp]),
     "eqlin_selftest_wait_timeout": (_i, [ctypes.c_uint64, _i, _vp, _vp]),
 }
 
@@ -386,6 +405,194 @@ def d8_fourier_mlp(z: torch.Tensor, W1pack: torch.Tensor, W2pack: torch.Tensor, 
                                       workspace.numel() if workspace is not None else 0, _stream_ptr(z.device))
     _check(rc, "eqlin_d8_fourier_mlp_ws")
     return y
+
+
+# ------------------------------------------------------------------ gated feed-forward
+
+
+def _run(where: str, device: torch.device, *args):
+    """Call the entry point `where` with the tensors' device current, on that
+    device's current stream."""
+    fn = getattr(_lib, where)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, _stream_ptr(device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream_ptr(device))
+    _check(rc, where)
+
+
+def _on(device: torch.device, t: torch.Tensor, name: str):
+    """The address of t, which must be contiguous and on `device`."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return _dev_ptr(t, name)
+
+
+def _given(t: torch.Tensor | None, shape, dtype: torch.dtype, device: torch.device, name: str) -> torch.Tensor:
+    """An output of this shape: the caller's tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} has the wrong shape or dtype")
+    return t
+
+
+def _scratch(workspace: torch.Tensor | None, need: int, device: torch.device):
+    """(address, bytes, tensor) of a workspace: the caller's or a new one."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a byte (uint8) tensor")
+    return _on(device, workspace, "workspace"), workspace.numel(), workspace
+
+
+def _gated_weight(W: torch.Tensor):
+    if W.dim() != 4 or W.shape[1] != 2:
+        raise ValueError("W must be [H, 2, Cin, N] (row (j, 0) the gate, (j, 1) the value)")
+    H, _, Cin, N = W.shape
+    return H, Cin, N
+
+
+def cyclic_gated_auto_path(N: int, Cin: int, H: int, dtype: torch.dtype) -> int:
+    return int(_lib.eqlin_cyclic_gated_auto_path(N, Cin, H, dtype_code(dtype)))
+
+
+def cyclic_gated_weight_spectrum(W: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """W [H, 2, Cin, N] (device; row (j, 0) field j's gate, (j, 1) its value) ->
+    opaque spectrum buffer of the gated layer."""
+    H, Cin, N = _gated_weight(W)
+    need = int(_lib.eqlin_cyclic_gated_spectrum_bytes(N, Cin, H, dtype_code(W.dtype)))
+    if need == 0:
+        raise EqlinError(EQLIN_ERR_UNSUPPORTED, "eqlin_cyclic_gated_spectrum_bytes")
+    if out is None:
+        out = torch.empty(need, dtype=torch.uint8, device=W.device)
+    _run("eqlin_cyclic_gated_weight_spectrum", W.device, _dev_ptr(W, "W"), N, Cin, H, dtype_code(W.dtype),
+         _on(W.device, out, "Wspec"), out.numel())
+    return out
+
+
+def cyclic_gated_weight_spectrum_adjoint(W: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """W [H, 2, Cin, N] (device) -> opaque spectrum that the gated layer's dx needs."""
+    H, Cin, N = _gated_weight(W)
+    need = int(_lib.eqlin_cyclic_gated_adjoint_bytes(N, Cin, H, dtype_code(W.dtype)))
+    if need == 0:
+        raise EqlinError(EQLIN_ERR_UNSUPPORTED, "eqlin_cyclic_gated_adjoint_bytes")
+    if out is None:
+        out = torch.empty(need, dtype=torch.uint8, device=W.device)
+    _run("eqlin_cyclic_gated_weight_spectrum_adjoint", W.device, _dev_ptr(W, "W"), N, Cin, H,
+         dtype_code(W.dtype), _on(W.device, out, "Wspec_adj"), out.numel())
+    return out
+
+
+def _spectrum_ptr(device: torch.device, spec: torch.Tensor, need: int, name: str):
+    if spec.dtype != torch.uint8 or spec.numel() < need or need == 0:
+        raise ValueError(f"{name} is not a spectrum of this layer (a byte tensor of at least {need} bytes)")
+    return _on(device, spec, name)
+
+
+def cyclic_gated_forward(x: torch.Tensor, Wspec: torch.Tensor, H: int, act: int = ACT_SILU,
+                         h: torch.Tensor | None = None, path: int = PATH_AUTO) -> torch.Tensor:
+    """x [T, Cin, N] (device) -> h [T, H, N] = act(gate) * value, gate and value
+    the two cyclic layers of W (see cyclic_gated_weight_spectrum)."""
+    T, Cin, N = x.shape
+    dt, dev = dtype_code(x.dtype), x.device
+    h = _given(h, (T, H, N), x.dtype, dev, "h")
+    spec = _spectrum_ptr(dev, Wspec, int(_lib.eqlin_cyclic_gated_spectrum_bytes(N, Cin, H, dt)), "Wspec")
+    _run("eqlin_cyclic_gated_forward", dev, _dev_ptr(x, "x"), spec, _on(dev, h, "h"), T, N, Cin, H, act, dt, path)
+    return h
+
+
+def cyclic_gated_backward_workspace_bytes(T: int, N: int, Cin: int, H: int, dtype: torch.dtype) -> int:
+    return int(_lib.eqlin_cyclic_gated_backward_workspace_bytes(T, N, Cin, H, dtype_code(dtype)))
+
+
+def cyclic_gated_backward(x: torch.Tensor, dh: torch.Tensor, Wspec: torch.Tensor, Wspec_adj: torch.Tensor,
+                          act: int = ACT_SILU, dx: torch.Tensor | None = None, dW: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, path: int = PATH_AUTO):
+    """Gradients of sum(dh * cyclic_gated_forward(x)): dx [T, Cin, N] and
+    dW [H, 2, Cin, N].  The workspace (a device byte tensor of
+    cyclic_gated_backward_workspace_bytes) is allocated here when not given."""
+    T, Cin, N = x.shape
+    if dh.dim() != 3 or dh.shape[0] != T or dh.shape[2] != N or dh.dtype != x.dtype:
+        raise ValueError("dh has the wrong shape or dtype")
+    H = dh.shape[1]
+    dt, dev = dtype_code(x.dtype), x.device
+    dx = _given(dx, (T, Cin, N), x.dtype, dev, "dx")
+    dW = _given(dW, (H, 2, Cin, N), x.dtype, dev, "dW")
+    spec = _spectrum_ptr(dev, Wspec, int(_lib.eqlin_cyclic_gated_spectrum_bytes(N, Cin, H, dt)), "Wspec")
+    adj = _spectrum_ptr(dev, Wspec_adj, int(_lib.eqlin_cyclic_gated_adjoint_bytes(N, Cin, H, dt)), "Wspec_adj")
+    ws, ws_bytes, _ = _scratch(workspace, cyclic_gated_backward_workspace_bytes(T, N, Cin, H, x.dtype), dev)
+    _run("eqlin_cyclic_gated_backward", dev, _dev_ptr(x, "x"), _on(dev, dh, "dh"), spec, adj, _on(dev, dx, "dx"),
+         _on(dev, dW, "dW"), T, N, Cin, H, act, dt, path, ws, ws_bytes)
+    return dx, dW
+
+
+# ------------------------------------------------------------------ group norm
+
+
+def _norm_shape(x: torch.Tensor):
+    if x.dim() < 3:
+        raise ValueError("x must be [B, positions..., F, N]")
+    B, F, N = x.shape[0], x.shape[-2], x.shape[-1]
+    S = 1
+    for d in x.shape[1:-2]:
+        S *= d
+    return B, S, F, N
+
+
+def _affine_ptr(p: torch.Tensor | None, F: int, x: torch.Tensor, name: str):
+    if p is None:
+        return None
+    if p.shape != (F,) or p.dtype != x.dtype:
+        raise ValueError(f"{name} must be [F] of x's dtype")
+    return _on(x.device, p, name)
+
+
+def group_norm(x: torch.Tensor, groups: int, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+               eps: float = 1e-5, act: int = ACT_NONE, y: torch.Tensor | None = None,
+               mean: torch.Tensor | None = None, rstd: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None):
+    """x [B, positions..., F, N] (device; [T, F, N] for tokens) ->
+    (y, mean, rstd): the group norm over each item's positions and the F / groups
+    fields of a group, y = act(gamma[f] * xhat + beta[f]) and fp32 mean, rstd
+    [B, groups] for group_norm_backward."""
+    B, S, F, N = _norm_shape(x)
+    dt, dev = dtype_code(x.dtype), x.device
+    y = _given(y, x.shape, x.dtype, dev, "y")
+    mean = _given(mean, (B, groups), torch.float32, dev, "mean")
+    rstd = _given(rstd, (B, groups), torch.float32, dev, "rstd")
+    ws, ws_bytes, _ = _scratch(workspace, int(_lib.eqlin_group_norm_workspace_bytes(B, S, F, N, groups, dt)), dev)
+    _run("eqlin_group_norm", dev, _dev_ptr(x, "x"), _affine_ptr(gamma, F, x, "gamma"),
+         _affine_ptr(beta, F, x, "beta"), _on(dev, y, "y"), _on(dev, mean, "mean"), _on(dev, rstd, "rstd"),
+         B, S, F, N, groups, eps, act, dt, ws, ws_bytes)
+    return y, mean, rstd
+
+
+def group_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, groups: int,
+                        gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None, act: int = ACT_NONE,
+                        dx: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Gradients of sum(dy * y) for group_norm: (dx, dgamma, dbeta), dgamma and
+    dbeta None where gamma and beta are."""
+    B, S, F, N = _norm_shape(x)
+    dt, dev = dtype_code(x.dtype), x.device
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy has the wrong shape or dtype")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t.shape != (B, groups) or t.dtype != torch.float32:
+            raise ValueError(f"{name} must be fp32 [B, groups]")
+    dx = _given(dx, x.shape, x.dtype, dev, "dx")
+    dgamma = torch.empty_like(gamma) if gamma is not None else None
+    dbeta = torch.empty_like(beta) if beta is not None else None
+    ws, ws_bytes, _ = _scratch(
+        workspace, int(_lib.eqlin_group_norm_backward_workspace_bytes(B, S, F, N, groups, dt)), dev)
+    _run("eqlin_group_norm_backward", dev, _dev_ptr(x, "x"), _on(dev, dy, "dy"), _on(dev, mean, "mean"),
+         _on(dev, rstd, "rstd"), _affine_ptr(gamma, F, x, "gamma"), _affine_ptr(beta, F, x, "beta"),
+         _on(dev, dx, "dx"), _affine_ptr(dgamma, F, x, "dgamma"), _affine_ptr(dbeta, F, x, "dbeta"),
+         B, S, F, N, groups, act, dt, ws, ws_bytes)
+    return dx, dgamma, dbeta
 
 
 # ------------------------------------------------------------------ host-resident data

@@ -26,7 +26,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "--expt-relaxed-constexpr",
-    "-shared", "-cudart", "static",
+    "-shared", "-cudart", "static", "--threads", "0",   # the sources side by side
 ]
 
 

@@ -1,0 +1,167 @@
+// Host side of the gated cyclic feed-forward layer: checks, buffer layouts and
+// the order of the passes.  Every check happens before a launch.
+#include "gated_internal.cuh"
+
+namespace eqlin {
+namespace {
+
+size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+bool aligned(const void *p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+int check_shape(int N, int Cin, int H, int dtype) {
+  if (H < 1 || H > (1 << 23)) return set_error(EQLIN_ERR_INVALID_ARG, "H=%d not in 1..2^23", H);
+  return check_cyclic_shape(N, Cin, 2 * H, dtype);
+}
+
+int check_call(int64_t T, int N, int Cin, int H, int act, int path) {
+  if (T < 0) return set_error(EQLIN_ERR_INVALID_ARG, "T=%lld < 0", (long long)T);
+  const int64_t widest = (int64_t)(Cin > 2 * H ? Cin : 2 * H) * N;
+  if (T > ((int64_t)1 << 58) / widest)   // byte offsets stay within 63 bits
+    return set_error(EQLIN_ERR_UNSUPPORTED, "T=%lld is too large", (long long)T);
+  if (act != EQLIN_ACT_NONE && act != EQLIN_ACT_SILU && act != EQLIN_ACT_GELU)
+    return set_error(EQLIN_ERR_INVALID_ARG, "unknown activation %d", act);
+  if (path != EQLIN_PATH_AUTO && path != EQLIN_PATH_SIMT && path != EQLIN_PATH_TC)
+    return set_error(EQLIN_ERR_INVALID_ARG, "unknown path %d", path);
+  return EQLIN_OK;
+}
+
+size_t elem_size(int dtype) { return dtype == EQLIN_F32 ? 4 : 2; }
+
+// The forward spectrum is that of the layer Cin -> 2H (rows (j, 0), (j, 1));
+// the adjoint that of 2H -> Cin.
+CyclicSpecLayout spec_layout(int N, int Cin, int H, int dtype) { return cyclic_spec_layout(N, Cin, 2 * H, dtype); }
+CyclicSpecLayout adjoint_layout(int N, int Cin, int H, int dtype) { return cyclic_spec_layout(N, 2 * H, Cin, dtype); }
+
+struct BackwardParts {
+  size_t dp, part, total;   // dp [T][2H][N] `dtype`; the weight gradient's partials
+};
+BackwardParts backward_parts(int64_t T, int N, int Cin, int H, int dtype) {
+  BackwardParts p{};
+  p.part = round256((size_t)T * 2 * H * N * elem_size(dtype));
+  p.total = p.part + round256(eqlin_cyclic_weight_grad_workspace_bytes(T, N, Cin, 2 * H, dtype));
+  return p;
+}
+
+int weight_spectrum(const void *W, int N, int Cin, int H, int dtype, bool adjoint, void *out, size_t bytes,
+                    cudaStream_t s) {
+  clear_error();
+  int rc = check_shape(N, Cin, H, dtype);
+  if (rc) return rc;
+  if (!W || !out) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(W, 16) || !aligned(out, 16)) return set_error(EQLIN_ERR_ALIGN, "W and the spectrum must be 16-byte aligned");
+  const CyclicSpecLayout L = adjoint ? adjoint_layout(N, Cin, H, dtype) : spec_layout(N, Cin, H, dtype);
+  if (bytes < L.total) return set_error(EQLIN_ERR_SIZE, "spectrum buffer of %zu bytes < required %zu", bytes, L.total);
+  return adjoint ? launch_cyclic_spectrum(W, N, 2 * H, Cin, dtype, 1, out, L, s)
+                 : launch_cyclic_spectrum(W, N, Cin, 2 * H, dtype, 0, out, L, s);
+}
+
+}  // namespace
+}  // namespace eqlin
+
+using namespace eqlin;
+
+extern "C" {
+
+size_t eqlin_cyclic_gated_spectrum_bytes(int N, int Cin, int H, int dtype) {
+  if (check_shape(N, Cin, H, dtype) != EQLIN_OK) return 0;
+  return spec_layout(N, Cin, H, dtype).total;
+}
+
+int eqlin_cyclic_gated_weight_spectrum(const void *W, int N, int Cin, int H, int dtype, void *Wspec,
+                                       size_t Wspec_bytes, eqlin_stream_t stream) {
+  return weight_spectrum(W, N, Cin, H, dtype, false, Wspec, Wspec_bytes, (cudaStream_t)stream);
+}
+
+size_t eqlin_cyclic_gated_adjoint_bytes(int N, int Cin, int H, int dtype) {
+  if (check_shape(N, Cin, H, dtype) != EQLIN_OK) return 0;
+  return adjoint_layout(N, Cin, H, dtype).total;
+}
+
+int eqlin_cyclic_gated_weight_spectrum_adjoint(const void *W, int N, int Cin, int H, int dtype, void *Wspec_adj,
+                                               size_t Wspec_adj_bytes, eqlin_stream_t stream) {
+  return weight_spectrum(W, N, Cin, H, dtype, true, Wspec_adj, Wspec_adj_bytes, (cudaStream_t)stream);
+}
+
+int eqlin_cyclic_gated_auto_path(int N, int Cin, int H, int dtype) {
+  if (check_shape(N, Cin, H, dtype) != EQLIN_OK) return -1;
+  return EQLIN_PATH_SIMT;
+}
+
+int eqlin_cyclic_gated_forward(const void *x, const void *Wspec, void *h, int64_t T, int N, int Cin, int H, int act,
+                               int dtype, int path, eqlin_stream_t stream) {
+  clear_error();
+  int rc = check_shape(N, Cin, H, dtype);
+  if (rc || (rc = check_call(T, N, Cin, H, act, path))) return rc;
+  if (path == EQLIN_PATH_TC) return set_error(EQLIN_ERR_UNSUPPORTED, "no tensor-core path for this layer");
+  if (T == 0) return EQLIN_OK;
+  if (!x || !Wspec || !h) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(x, 16) || !aligned(h, 16) || !aligned(Wspec, 16))
+    return set_error(EQLIN_ERR_ALIGN, "x, h and Wspec must be 16-byte aligned");
+  GatedIo io{};
+  io.x = x;
+  io.Ws = reinterpret_cast<const float *>(static_cast<const char *>(Wspec) + spec_layout(N, Cin, H, dtype).simt_offset);
+  io.out = h;
+  io.T = T;
+  io.Cin = Cin;
+  io.Cout = 2 * H;
+  return launch_gated_simt(kEpiGated, io, N, act, dtype, (cudaStream_t)stream);
+}
+
+size_t eqlin_cyclic_gated_backward_workspace_bytes(int64_t T, int N, int Cin, int H, int dtype) {
+  if (check_shape(N, Cin, H, dtype) != EQLIN_OK || T <= 0 ||
+      check_call(T, N, Cin, H, EQLIN_ACT_NONE, EQLIN_PATH_AUTO) != EQLIN_OK)
+    return 0;
+  return backward_parts(T, N, Cin, H, dtype).total;
+}
+
+int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec, const void *Wspec_adj, void *dx,
+                                void *dW, int64_t T, int N, int Cin, int H, int act, int dtype, int path,
+                                void *workspace, size_t workspace_bytes, eqlin_stream_t stream) {
+  clear_error();
+  const cudaStream_t s = (cudaStream_t)stream;
+  int rc = check_shape(N, Cin, H, dtype);
+  if (rc || (rc = check_call(T, N, Cin, H, act, path))) return rc;
+  if (path == EQLIN_PATH_TC) return set_error(EQLIN_ERR_UNSUPPORTED, "no tensor-core path for this layer");
+  if (!dx && !dW) return set_error(EQLIN_ERR_INVALID_ARG, "dx and dW are both null");
+  if (!aligned(dW, 16)) return set_error(EQLIN_ERR_ALIGN, "dW must be 16-byte aligned");
+  if (T == 0) {
+    if (dW && cudaMemsetAsync(dW, 0, (size_t)2 * H * Cin * N * elem_size(dtype), s) != cudaSuccess)
+      return check_launch("gated layer backward (no tokens)");
+    return EQLIN_OK;
+  }
+  if (!x || !dh || !Wspec || (dx && !Wspec_adj)) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(x, 16) || !aligned(dh, 16) || !aligned(dx, 16) || !aligned(Wspec, 16) || !aligned(Wspec_adj, 16))
+    return set_error(EQLIN_ERR_ALIGN, "x, dh, dx and the spectra must be 16-byte aligned");
+  const BackwardParts p = backward_parts(T, N, Cin, H, dtype);
+  if (!workspace) return set_error(EQLIN_ERR_INVALID_ARG, "null workspace");
+  if (workspace_bytes < p.total)
+    return set_error(EQLIN_ERR_SIZE, "workspace_bytes=%zu < required %zu", workspace_bytes, p.total);
+  if (!aligned(workspace, 256)) return set_error(EQLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
+  char *ws = static_cast<char *>(workspace);
+  GatedIo io{};
+  io.x = x;
+  io.Ws = reinterpret_cast<const float *>(static_cast<const char *>(Wspec) + spec_layout(N, Cin, H, dtype).simt_offset);
+  io.dh = dh;
+  io.out = ws + p.dp;
+  io.T = T;
+  io.Cin = Cin;
+  io.Cout = 2 * H;
+  if ((rc = launch_gated_simt(kEpiGates, io, N, act, dtype, s))) return rc;
+  if (dx) {
+    GatedIo b{};
+    b.x = ws + p.dp;
+    b.Ws = reinterpret_cast<const float *>(static_cast<const char *>(Wspec_adj) +
+                                           adjoint_layout(N, Cin, H, dtype).simt_offset);
+    b.out = dx;
+    b.T = T;
+    b.Cin = 2 * H;
+    b.Cout = Cin;
+    if ((rc = launch_gated_simt(kEpiLinear, b, N, EQLIN_ACT_NONE, dtype, s))) return rc;
+  }
+  if (!dW) return EQLIN_OK;
+  return eqlin_cyclic_weight_grad_ex(x, ws + p.dp, dW, T, N, Cin, 2 * H, dtype, ws + p.part,
+                                     workspace_bytes - p.part,
+                                     path == EQLIN_PATH_SIMT ? EQLIN_PATH_SIMT : EQLIN_PATH_AUTO, stream);
+}
+
+}  // extern "C"

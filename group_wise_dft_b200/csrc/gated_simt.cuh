@@ -1,0 +1,348 @@
+// CUDA-core kernels of the gated cyclic feed-forward layer: for every N in
+// 1..16, every channel count and fp32, bf16 or fp16.
+//
+// p[t,o,:] = sum_i W[o,i,:] * x[t,i,:] (circular convolution), computed through
+// the half spectra: forward real DFT of each field, per-bin products in fp32
+// against the fp32 weight spectrum, inverse DFT; the epilogue then gates
+// (rows 2j and 2j + 1 are field j's gate and value) without p reaching memory.
+//
+// Two kernels:
+//  - tiles: a CTA takes 8 kTPT tokens by 64 outputs.  A thread keeps 2 outputs
+//    x kTPT tokens x N coordinates in registers, so that one i costs 2 N weight
+//    loads (coalesced over the lanes) and kTPT N broadcast words of the shared
+//    spectrum for 2 kTPT (2N - 2) FMAs: the FMA pipe paces it, not the loads.
+//  - few tokens: with a handful of tokens the weights are what is read and
+//    only a wide split hides their latency: a CTA takes 8 outputs and splits
+//    the input fields 32 ways over its threads, joined in a fixed order.
+#pragma once
+
+#include "activations.cuh"
+#include "gated_internal.cuh"
+
+namespace eqlin {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int N> struct Tile {
+  static constexpr int NP = (N + 3) / 4 * 4;                    // coordinates per field in shared memory
+  static constexpr int TPT = N <= 4 ? 8 : 4;                    // tokens per thread
+  static constexpr int TT = 8 * TPT;                            // tokens per CTA
+  static constexpr int IC = N <= 8 ? 16 : 8;                    // input fields per shared-memory step
+  static constexpr int CTAS = N <= 8 ? 2 : 1;                   // per SM: up to 128 or 255 registers, no spills
+};
+
+template <int N>
+__device__ __forceinline__ void forward_dft(const DftTables &tab, const float (&v)[N], float (&X)[N]) {
+  if constexpr (N == 4) {
+    p4_forward(v, X);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      float s = 0.f;
+#pragma unroll
+      for (int h = 0; h < N; ++h) s = fmaf(tab.fwd[c][h], v[h], s);
+      X[c] = s;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void inverse_dft(const DftTables &tab, const float (&Y)[N], float (&y)[N]) {
+  if constexpr (N == 4) {
+    p4_inverse(Y, y);
+  } else {
+#pragma unroll
+    for (int g = 0; g < N; ++g) {
+      float s = 0.f;
+#pragma unroll
+      for (int c = 0; c < N; ++c) s = fmaf(tab.inv[g][c], Y[c], s);
+      y[g] = s;
+    }
+  }
+}
+
+// acc += w X per bin (coordinates as in DftTables)
+template <int N>
+__device__ __forceinline__ void bin_products(float (&acc)[N], const float (&w)[N], const float (&X)[N]) {
+  acc[0] = fmaf(w[0], X[0], acc[0]);
+#pragma unroll
+  for (int k = 1; 2 * k < N; ++k) {
+    const int cr = 2 * k - 1, ci = 2 * k;
+    acc[cr] = fmaf(w[cr], X[cr], fmaf(-w[ci], X[ci], acc[cr]));
+    acc[ci] = fmaf(w[cr], X[ci], fmaf(w[ci], X[cr], acc[ci]));
+  }
+  if (N % 2 == 0 && N > 1) acc[N - 1] = fmaf(w[N - 1], X[N - 1], acc[N - 1]);
+}
+
+// Epilogue of field j of token t from the coordinates of its gate and value.
+template <int N, typename T, int EPI>
+__device__ __forceinline__ void gate_store(const DftTables &tab, const float (&G)[N], const float (&U)[N],
+                                           const T *dh, T *out, int64_t t, int j, int H, int act) {
+  float g[N], u[N];
+  inverse_dft<N>(tab, G, g);
+  inverse_dft<N>(tab, U, u);
+  const size_t at = ((size_t)t * H + j) * N;
+  if constexpr (EPI == kEpiGated) {
+    float h[N];
+#pragma unroll
+    for (int s = 0; s < N; ++s) h[s] = act_any(act, g[s]) * u[s];
+    store_field<N, T>(out + at, h);
+  } else {
+    float d[N], dg[N], du[N];
+    load_field<N, T>(dh + at, d);
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+      float a;
+      const float slope = slope_any(act, g[s], a);
+      dg[s] = d[s] * u[s] * slope;
+      du[s] = d[s] * a;
+    }
+    store_field<N, T>(out + 2 * at, dg);
+    store_field<N, T>(out + 2 * at + N, du);
+  }
+}
+
+// A lane's two outputs: the pair (2j, 2j + 1) of field j, or for the plain
+// product two outputs 32 apart (any Cout, coalesced).
+template <int N, typename T, int EPI>
+__global__ void __launch_bounds__(kThreads, Tile<N>::CTAS)
+spectral_tile_kernel(const T *__restrict__ x, const float *__restrict__ Ws, const T *__restrict__ dh,
+                     T *__restrict__ out, int64_t Tn, int Cin, int Cout, int act, DftTables tab) {
+  using L = Tile<N>;
+  __shared__ __align__(16) float Xs[L::TT][L::IC][L::NP];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t0 = (int64_t)blockIdx.x * L::TT;
+  const int o0 = blockIdx.y * 64;
+  const int oa = EPI == kEpiLinear ? o0 + lane : o0 + 2 * lane;
+  const int ob = EPI == kEpiLinear ? oa + 32 : oa + 1;
+  const bool has_a = oa < Cout, has_b = ob < Cout;
+
+  float acc[2][L::TPT][N];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int a = 0; a < L::TPT; ++a)
+#pragma unroll
+      for (int c = 0; c < N; ++c) acc[p][a][c] = 0.f;
+
+  for (int i0 = 0; i0 < Cin; i0 += L::IC) {
+    __syncthreads();
+    for (int p = threadIdx.x; p < L::TT * L::IC; p += kThreads) {
+      const int tl = p / L::IC, il = p % L::IC;
+      const int64_t t = t0 + tl;
+      const int i = i0 + il;
+      float v[N], X[N];
+      if (t < Tn && i < Cin) {
+        load_field<N, T>(x + ((size_t)t * Cin + i) * N, v);
+      } else {
+#pragma unroll
+        for (int h = 0; h < N; ++h) v[h] = 0.f;
+      }
+      forward_dft<N>(tab, v, X);
+#pragma unroll
+      for (int c = 0; c < N; ++c) Xs[tl][il][c] = X[c];
+    }
+    __syncthreads();
+    const int iend = min(L::IC, Cin - i0);
+#pragma unroll 2
+    for (int il = 0; il < iend; ++il) {
+      float wa[N], wb[N];
+      const float *wp = Ws + (size_t)(i0 + il) * N * Cout;
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        if constexpr (EPI == kEpiLinear) {
+          wa[c] = has_a ? __ldg(wp + (size_t)c * Cout + oa) : 0.f;
+          wb[c] = has_b ? __ldg(wp + (size_t)c * Cout + ob) : 0.f;
+        } else {   // Cout is even: the pair is one aligned 8-byte word
+          const float2 w = has_a ? __ldg(reinterpret_cast<const float2 *>(wp + (size_t)c * Cout + oa))
+                                 : make_float2(0.f, 0.f);
+          wa[c] = w.x;
+          wb[c] = w.y;
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < L::TPT; ++a) {
+        const float4 *src = reinterpret_cast<const float4 *>(Xs[warp * L::TPT + a][il]);
+        float X[N];
+#pragma unroll
+        for (int c = 0; c < N; c += 4) {
+          const float4 q = src[c / 4];
+          X[c] = q.x;
+          if (c + 1 < N) X[c + 1] = q.y;
+          if (c + 2 < N) X[c + 2] = q.z;
+          if (c + 3 < N) X[c + 3] = q.w;
+        }
+        bin_products<N>(acc[0][a], wa, X);
+        bin_products<N>(acc[1][a], wb, X);
+      }
+    }
+  }
+  if (!has_a) return;
+#pragma unroll
+  for (int a = 0; a < L::TPT; ++a) {
+    const int64_t t = t0 + warp * L::TPT + a;
+    if (t >= Tn) continue;
+    if constexpr (EPI == kEpiLinear) {
+      float y[N];
+      inverse_dft<N>(tab, acc[0][a], y);
+      store_field<N, T>(out + ((size_t)t * Cout + oa) * N, y);
+      if (has_b) {
+        inverse_dft<N>(tab, acc[1][a], y);
+        store_field<N, T>(out + ((size_t)t * Cout + ob) * N, y);
+      }
+    } else {
+      gate_store<N, T, EPI>(tab, acc[0][a], acc[1][a], dh, out, t, oa >> 1, Cout >> 1, act);
+    }
+  }
+}
+
+// ------------------------------------------------------------ few tokens
+
+constexpr int kFewOut = 8;       // outputs per CTA: 4 lanes of a warp share one
+constexpr int kFewSplit = kThreads / kFewOut;   // ways the input fields are split
+constexpr int kFewIC = 128;      // input fields per shared-memory step
+template <int N> constexpr int few_tokens() { return N <= 8 ? 4 : 2; }   // tokens per CTA
+
+template <int N, typename T, int EPI>
+__global__ void __launch_bounds__(kThreads)
+spectral_few_kernel(const T *__restrict__ x, const float *__restrict__ Ws, const T *__restrict__ dh,
+                    T *__restrict__ out, int64_t Tn, int Cin, int Cout, int act, DftTables tab) {
+  constexpr int TB = few_tokens<N>();
+  // the spectra of a step's fields, then the warps' partial sums
+  __shared__ __align__(16) float sm[kFewIC * TB * N];
+  static_assert(8 * kFewOut * TB * N <= kFewIC * TB * N, "the partial sums fit");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ol = lane & (kFewOut - 1);
+  const int part = warp * (32 / kFewOut) + lane / kFewOut;
+  const int o = blockIdx.x * kFewOut + ol;
+  const int64_t t0 = (int64_t)blockIdx.y * TB;
+  float acc[TB][N];
+#pragma unroll
+  for (int a = 0; a < TB; ++a)
+#pragma unroll
+    for (int c = 0; c < N; ++c) acc[a][c] = 0.f;
+  for (int i0 = 0; i0 < Cin; i0 += kFewIC) {
+    const int ni = min(kFewIC, Cin - i0);
+    __syncthreads();
+    for (int p = threadIdx.x; p < ni * TB; p += kThreads) {
+      const int il = p % ni, a = p / ni;
+      float v[N], X[N];
+      if (t0 + a < Tn) {
+        load_field<N, T>(x + ((size_t)(t0 + a) * Cin + i0 + il) * N, v);
+      } else {
+#pragma unroll
+        for (int h = 0; h < N; ++h) v[h] = 0.f;
+      }
+      forward_dft<N>(tab, v, X);
+#pragma unroll
+      for (int c = 0; c < N; ++c) sm[(il * TB + a) * N + c] = X[c];
+    }
+    __syncthreads();
+    if (o < Cout)
+#pragma unroll 2
+      for (int il = part; il < ni; il += kFewSplit) {
+        float w[N];
+        const float *wp = Ws + (size_t)(i0 + il) * N * Cout + o;
+#pragma unroll
+        for (int c = 0; c < N; ++c) w[c] = __ldg(wp + (size_t)c * Cout);
+#pragma unroll
+        for (int a = 0; a < TB; ++a) {
+          float X[N];
+#pragma unroll
+          for (int c = 0; c < N; ++c) X[c] = sm[(il * TB + a) * N + c];
+          bin_products<N>(acc[a], w, X);
+        }
+      }
+  }
+  // join the 4 lanes of an output, then the 8 warps in order
+#pragma unroll
+  for (int a = 0; a < TB; ++a)
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      acc[a][c] += __shfl_xor_sync(0xffffffffu, acc[a][c], kFewOut);
+      acc[a][c] += __shfl_xor_sync(0xffffffffu, acc[a][c], 2 * kFewOut);
+    }
+  __syncthreads();
+  if (lane < kFewOut)
+#pragma unroll
+    for (int a = 0; a < TB; ++a)
+#pragma unroll
+      for (int c = 0; c < N; ++c) sm[((warp * kFewOut + ol) * TB + a) * N + c] = acc[a][c];
+  __syncthreads();
+  auto joined = [&](int out_l, int a, float(&v)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) v[c] = 0.f;
+    for (int w = 0; w < kThreads / 32; ++w)
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[c] += sm[((w * kFewOut + out_l) * TB + a) * N + c];
+  };
+  if constexpr (EPI == kEpiLinear) {
+    const int a = threadIdx.x / kFewOut, q = threadIdx.x % kFewOut;
+    const int oo = blockIdx.x * kFewOut + q;
+    if (a < TB && oo < Cout && t0 + a < Tn) {
+      float v[N], y[N];
+      joined(q, a, v);
+      inverse_dft<N>(tab, v, y);
+      store_field<N, T>(out + ((size_t)(t0 + a) * Cout + oo) * N, y);
+    }
+  } else {
+    const int a = threadIdx.x / (kFewOut / 2), q = threadIdx.x % (kFewOut / 2);
+    const int oo = blockIdx.x * kFewOut + 2 * q;
+    if (a < TB && oo < Cout && t0 + a < Tn) {
+      float G[N], U[N];
+      joined(2 * q, a, G);
+      joined(2 * q + 1, a, U);
+      gate_store<N, T, EPI>(tab, G, U, dh, out, t0 + a, oo >> 1, Cout >> 1, act);
+    }
+  }
+}
+
+// Tokens up to which the few-token kernel runs.
+constexpr int64_t kFewTokensMost = 32;
+
+template <int N, typename T, int EPI>
+int launch_ne(const GatedIo &io, int act, const DftTables &tab, cudaStream_t s) {
+  if (io.T <= kFewTokensMost) {
+    const dim3 grid((unsigned)((io.Cout + kFewOut - 1) / kFewOut),
+                    (unsigned)((io.T + few_tokens<N>() - 1) / few_tokens<N>()));
+    spectral_few_kernel<N, T, EPI><<<grid, kThreads, 0, s>>>((const T *)io.x, io.Ws, (const T *)io.dh,
+                                                                  (T *)io.out, io.T, io.Cin, io.Cout, act, tab);
+    return check_launch("gated layer (few tokens)");
+  }
+  const int64_t gx = (io.T + Tile<N>::TT - 1) / Tile<N>::TT;
+  const int64_t gy = ((int64_t)io.Cout + 63) / 64;
+  if (gx > 0x7fffffffLL) return set_error(EQLIN_ERR_UNSUPPORTED, "T too large for the CUDA-core grid");
+  if (gy > 65535) return set_error(EQLIN_ERR_UNSUPPORTED, "channel count too large for the CUDA-core grid");
+  spectral_tile_kernel<N, T, EPI><<<dim3((unsigned)gx, (unsigned)gy), kThreads, 0, s>>>(
+      (const T *)io.x, io.Ws, (const T *)io.dh, (T *)io.out, io.T, io.Cin, io.Cout, act, tab);
+  return check_launch("gated layer");
+}
+
+template <int N, typename T>
+int launch_n(int epi, const GatedIo &io, int act, const DftTables &tab, cudaStream_t s) {
+  return epi == kEpiLinear  ? launch_ne<N, T, kEpiLinear>(io, act, tab, s)
+         : epi == kEpiGated ? launch_ne<N, T, kEpiGated>(io, act, tab, s)
+                            : launch_ne<N, T, kEpiGates>(io, act, tab, s);
+}
+
+}  // namespace
+
+// T is fixed by the including unit, so that the three types build side by side.
+template <>
+int launch_gated_simt_t<EQLIN_GATED_TYPE>(int epi, const GatedIo &io, int N, int act, cudaStream_t s) {
+  DftTables tab;
+  make_dft_tables(N, &tab);
+  switch (N) {
+#define EQLIN_CASE(NN) \
+  case NN:             \
+    return launch_n<NN, EQLIN_GATED_TYPE>(epi, io, act, tab, s);
+    EQLIN_CASE(1) EQLIN_CASE(2) EQLIN_CASE(3) EQLIN_CASE(4) EQLIN_CASE(5) EQLIN_CASE(6)
+    EQLIN_CASE(7) EQLIN_CASE(8) EQLIN_CASE(9) EQLIN_CASE(10) EQLIN_CASE(11) EQLIN_CASE(12)
+    EQLIN_CASE(13) EQLIN_CASE(14) EQLIN_CASE(15) EQLIN_CASE(16)
+#undef EQLIN_CASE
+    default:
+      return set_error(EQLIN_ERR_UNSUPPORTED, "N=%d not in 1..16", N);
+  }
+}
+
+}  // namespace eqlin

@@ -83,6 +83,13 @@ enum {
   EQLIN_PATH_TC = 2     /* tcgen05 tensor-core path (bf16, see below)       */
 };
 
+/* Pointwise activations of the group norm and of the gated layer. */
+enum {
+  EQLIN_ACT_NONE = 0,
+  EQLIN_ACT_SILU = 1,   /* z / (1 + exp(-z))                 */
+  EQLIN_ACT_GELU = 2    /* 0.5 z (1 + erf(z / sqrt 2))       */
+};
+
 /* Message for the last error returned on this thread ("" if none). */
 EQLIN_API const char *eqlin_last_error(void);
 
@@ -343,6 +350,85 @@ EQLIN_API int eqlin_d8_fourier_mlp_ws(const void *z, const void *W1pack, const v
                             size_t workspace_bytes, eqlin_stream_t stream);
 EQLIN_API int eqlin_d8_fourier_mlp(const void *z, const void *W1pack, const void *W2pack, void *hidden,
                          void *y, int64_t T, int F, int F_hidden, int dtype, eqlin_stream_t stream);
+
+/* ------------------------------------------------- gated feed-forward */
+
+/* Gated feed-forward layer over C_N: both projections, the activation and the
+ * product in one pass,
+ *     p[t, j, a, g] = sum_i sum_h W[j, a, i, (g - h) mod N] x[t, i, h],
+ *     h[t, j, g] = act(p[t, j, 0, g]) p[t, j, 1, g].
+ * It is equivariant: act and the product are pointwise in the regular domain.
+ * x: device [T][Cin][N]; W: device [H][2][Cin][N], row (j, 0) field j's gate
+ * and row (j, 1) its value; h: device [T][H][N]; act: EQLIN_ACT_*; all `dtype`.
+ *
+ * eqlin_cyclic_gated_weight_spectrum writes W's half spectrum (opaque) for the
+ * forward and for the backward's recomputation, and
+ * eqlin_cyclic_gated_weight_spectrum_adjoint the one that dx needs; both once
+ * per weight.  Spectra are read back for the same (N, Cin, H, dtype) only.
+ *
+ * eqlin_cyclic_gated_backward: the gradients of sum(dh * h).  p is computed
+ * again (the forward keeps nothing), then
+ *     dp[t, j, 0] = dh p[t, j, 1] act'(p[t, j, 0]),  dp[t, j, 1] = dh act(p[t, j, 0])
+ * go, rounded to `dtype`, to the workspace, and from them
+ *     dx[t, i, h] = sum_j sum_a sum_g W[j, a, i, (g - h) mod N] dp[t, j, a, g],
+ *     dW[j, a, i, m] = sum_t sum_g dp[t, j, a, g] x[t, i, (g - m) mod N].
+ * dh: device [T][H][N]; dx: device [T][Cin][N]; dW: device [H][2][Cin][N]
+ * (overwritten).  dx or dW may be NULL (not computed; Wspec_adj may be NULL
+ * without dx).  The weight gradient's token partials are summed in a fixed
+ * order.  T = 0: dW = 0.
+ * The workspaces are caller-owned device memory, 256-byte aligned, of at least
+ * the *_workspace_bytes; their contents on entry do not matter.  Calls that
+ * may overlap on the GPU need one each.
+ *
+ * Supported: 1 <= N <= 16, Cin, H >= 1, every dtype.  EQLIN_PATH_SIMT runs on
+ * CUDA cores in fp32.  EQLIN_PATH_TC returns EQLIN_ERR_UNSUPPORTED where
+ * eqlin_cyclic_gated_auto_path says EQLIN_PATH_SIMT. */
+EQLIN_API size_t eqlin_cyclic_gated_spectrum_bytes(int N, int Cin, int H, int dtype);
+EQLIN_API int eqlin_cyclic_gated_weight_spectrum(const void *W, int N, int Cin, int H, int dtype, void *Wspec,
+                                       size_t Wspec_bytes, eqlin_stream_t stream);
+EQLIN_API size_t eqlin_cyclic_gated_adjoint_bytes(int N, int Cin, int H, int dtype);
+EQLIN_API int eqlin_cyclic_gated_weight_spectrum_adjoint(const void *W, int N, int Cin, int H, int dtype,
+                                               void *Wspec_adj, size_t Wspec_adj_bytes, eqlin_stream_t stream);
+EQLIN_API int eqlin_cyclic_gated_auto_path(int N, int Cin, int H, int dtype);
+EQLIN_API int eqlin_cyclic_gated_forward(const void *x, const void *Wspec, void *h, int64_t T, int N, int Cin,
+                               int H, int act, int dtype, int path, eqlin_stream_t stream);
+EQLIN_API size_t eqlin_cyclic_gated_backward_workspace_bytes(int64_t T, int N, int Cin, int H, int dtype);
+EQLIN_API int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec, const void *Wspec_adj,
+                                void *dx, void *dW, int64_t T, int N, int Cin, int H, int act, int dtype,
+                                int path, void *workspace, size_t workspace_bytes, eqlin_stream_t stream);
+
+/* ---------------------------------------------------------- group norm */
+
+/* Group norm with a pointwise activation, channels last, for activations in
+ * the regular representation (C_N, or D8 with N = 8):
+ *     x, y: device [B][S][F][N] (B items of S positions, F fields),
+ *     mean[b, g], var[b, g] over the S (F / G) N values of item b, group g
+ *     (G groups of F / G consecutive fields; biased variance),
+ *     y = act(gamma[f] (x - mean) rstd + beta[f]),  rstd = 1 / sqrt(var + eps).
+ * gamma and beta (device [F], `dtype`; NULL: 1 and 0) are constant along the
+ * group axis and the statistics are invariant under the group, so the layer
+ * is equivariant.  S = 1 normalises tokens (G = 1: layer norm).  mean and rstd
+ * (device fp32 [B][G]) are written for the backward pass; either may be NULL.
+ * fp32 statistics and arithmetic.  S = 0 or B = 0 does nothing.
+ *
+ * Backward: from dy and the forward's mean and rstd, with dz = dy act'(z),
+ *     dbeta[f] = sum dz,  dgamma[f] = sum dz xhat,
+ *     dx = rstd (gamma dz - E[gamma dz] - xhat E[gamma dz xhat])  (E over the group).
+ * dgamma and dbeta (device [F], `dtype`) may be NULL; they are 0 when there
+ * are no values.  Sums have a fixed order.
+ *
+ * Supported: 1 <= N <= 16, F a multiple of G, G <= 2048, F * N <= 2^24, every
+ * dtype.  eps >= 0.  Workspaces as above, 16-byte aligned, of at least the
+ * *_workspace_bytes (0 when none is needed: then it may be NULL). */
+EQLIN_API size_t eqlin_group_norm_workspace_bytes(int64_t B, int64_t S, int F, int N, int G, int dtype);
+EQLIN_API int eqlin_group_norm(const void *x, const void *gamma, const void *beta, void *y, float *mean, float *rstd,
+                     int64_t B, int64_t S, int F, int N, int G, float eps, int act, int dtype,
+                     void *workspace, size_t workspace_bytes, eqlin_stream_t stream);
+EQLIN_API size_t eqlin_group_norm_backward_workspace_bytes(int64_t B, int64_t S, int F, int N, int G, int dtype);
+EQLIN_API int eqlin_group_norm_backward(const void *x, const void *dy, const float *mean, const float *rstd,
+                              const void *gamma, const void *beta, void *dx, void *dgamma, void *dbeta,
+                              int64_t B, int64_t S, int F, int N, int G, int act, int dtype,
+                              void *workspace, size_t workspace_bytes, eqlin_stream_t stream);
 
 #ifdef __cplusplus
 }
