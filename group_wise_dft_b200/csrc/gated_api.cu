@@ -13,6 +13,8 @@ int check_shape(int N, int Cin, int H, int dtype) {
   return check_cyclic_shape(N, Cin, 2 * H, dtype);
 }
 
+const char *kTcNeeds = "the gated layer's tensor-core path needs bf16 or fp16, N=8, Cin%%16==0 (16..160) and H%%16==0";
+
 int check_call(int64_t T, int N, int Cin, int H, int act, int path) {
   if (T < 0) return set_error(EQLIN_ERR_INVALID_ARG, "T=%lld < 0", (long long)T);
   const int64_t widest = (int64_t)(Cin > 2 * H ? Cin : 2 * H) * N;
@@ -27,10 +29,39 @@ int check_call(int64_t T, int N, int Cin, int H, int act, int path) {
 
 size_t elem_size(int dtype) { return dtype == EQLIN_F32 ? 4 : 2; }
 
-// The forward spectrum is that of the layer Cin -> 2H (rows (j, 0), (j, 1));
-// the adjoint that of 2H -> Cin.
-CyclicSpecLayout spec_layout(int N, int Cin, int H, int dtype) { return cyclic_spec_layout(N, Cin, 2 * H, dtype); }
-CyclicSpecLayout adjoint_layout(int N, int Cin, int H, int dtype) { return cyclic_spec_layout(N, 2 * H, Cin, dtype); }
+// A spectrum buffer: the fp32 half spectrum Ws[i][c][o] of the CUDA-core kernels,
+// then, for the layers that have a tensor-core form, its packed weights.  The
+// forward's is the layer Cin -> 2H (rows (j, 0), (j, 1)), the adjoint 2H -> Cin.
+struct SpecLayout {
+  size_t tc_offset, tc_bytes, total;
+};
+SpecLayout layout(int N, int F_in, int F_out, size_t tc_bytes) {
+  SpecLayout L;
+  L.tc_offset = round256((size_t)F_in * N * F_out * sizeof(float));
+  L.tc_bytes = tc_bytes;
+  L.total = L.tc_offset + tc_bytes;
+  return L;
+}
+bool tc_supported(int N, int Cin, int H, int dtype) {
+  return cyclic_tc_supported(N, Cin, 2 * H, dtype) || cyclic_tc_f16_supported(N, Cin, 2 * H, dtype);
+}
+SpecLayout spec_layout(int N, int Cin, int H, int dtype) {
+  return layout(N, Cin, 2 * H, tc_supported(N, Cin, H, dtype) ? cyclic_tc_bytes(N, Cin, 2 * H) : 0);
+}
+SpecLayout adjoint_layout(int N, int Cin, int H, int dtype) {
+  return layout(N, 2 * H, Cin, tc_supported(N, Cin, H, dtype) ? wide_tc_bytes(2 * H, Cin) : 0);
+}
+const float *fp32_section(const void *spec) { return static_cast<const float *>(spec); }
+const void *tc_section(const void *spec, const SpecLayout &L) { return static_cast<const char *>(spec) + L.tc_offset; }
+
+// Few tokens go to the CUDA cores: they spread the weights' reading over the
+// whole GPU, where one tile of the tensor-core kernel would keep a single pair
+// of SMs busy.
+constexpr int64_t kTcTokensLeast = 33;
+bool use_tc(int64_t T, int N, int Cin, int H, int dtype, int path) {
+  if (!tc_supported(N, Cin, H, dtype) || path == EQLIN_PATH_SIMT) return false;
+  return path == EQLIN_PATH_TC || (dtype == EQLIN_BF16 && T >= kTcTokensLeast);
+}
 
 struct BackwardParts {
   size_t dp, part, total;   // dp [T][2H][N] `dtype`; the weight gradient's partials
@@ -49,10 +80,16 @@ int weight_spectrum(const void *W, int N, int Cin, int H, int dtype, bool adjoin
   if (rc) return rc;
   if (!W || !out) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
   if (!aligned(W, 16) || !aligned(out, 16)) return set_error(EQLIN_ERR_ALIGN, "W and the spectrum must be 16-byte aligned");
-  const CyclicSpecLayout L = adjoint ? adjoint_layout(N, Cin, H, dtype) : spec_layout(N, Cin, H, dtype);
+  const SpecLayout L = adjoint ? adjoint_layout(N, Cin, H, dtype) : spec_layout(N, Cin, H, dtype);
   if (bytes < L.total) return set_error(EQLIN_ERR_SIZE, "spectrum buffer of %zu bytes < required %zu", bytes, L.total);
-  return adjoint ? launch_cyclic_spectrum(W, N, 2 * H, Cin, dtype, 1, out, L, s)
-                 : launch_cyclic_spectrum(W, N, Cin, 2 * H, dtype, 0, out, L, s);
+  if (L.tc_bytes) {
+    char *tc = static_cast<char *>(out) + L.tc_offset;
+    return adjoint ? launch_wide_tc_pack(W, 2 * H, Cin, true, dtype, out, tc, s)
+                   : launch_gated_tc_pack(W, Cin, 2 * H, dtype, out, tc, s);
+  }
+  CyclicSpecLayout C{};   // the fp32 section alone
+  return adjoint ? launch_cyclic_spectrum(W, N, 2 * H, Cin, dtype, 1, out, C, s)
+                 : launch_cyclic_spectrum(W, N, Cin, 2 * H, dtype, 0, out, C, s);
 }
 
 }  // namespace
@@ -84,7 +121,7 @@ int eqlin_cyclic_gated_weight_spectrum_adjoint(const void *W, int N, int Cin, in
 
 int eqlin_cyclic_gated_auto_path(int N, int Cin, int H, int dtype) {
   if (check_shape(N, Cin, H, dtype) != EQLIN_OK) return -1;
-  return EQLIN_PATH_SIMT;
+  return tc_supported(N, Cin, H, dtype) && dtype == EQLIN_BF16 ? EQLIN_PATH_TC : EQLIN_PATH_SIMT;
 }
 
 int eqlin_cyclic_gated_forward(const void *x, const void *Wspec, void *h, int64_t T, int N, int Cin, int H, int act,
@@ -92,14 +129,17 @@ int eqlin_cyclic_gated_forward(const void *x, const void *Wspec, void *h, int64_
   clear_error();
   int rc = check_shape(N, Cin, H, dtype);
   if (rc || (rc = check_call(T, N, Cin, H, act, path))) return rc;
-  if (path == EQLIN_PATH_TC) return set_error(EQLIN_ERR_UNSUPPORTED, "no tensor-core path for this layer");
+  if (path == EQLIN_PATH_TC && !tc_supported(N, Cin, H, dtype)) return set_error(EQLIN_ERR_UNSUPPORTED, kTcNeeds);
   if (T == 0) return EQLIN_OK;
   if (!x || !Wspec || !h) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
   if (!aligned(x, 16) || !aligned(h, 16) || !aligned(Wspec, 16))
     return set_error(EQLIN_ERR_ALIGN, "x, h and Wspec must be 16-byte aligned");
+  if (use_tc(T, N, Cin, H, dtype, path))
+    return launch_gated_tc(kEpiGated, x, tc_section(Wspec, spec_layout(N, Cin, H, dtype)), nullptr, h, T, Cin, 2 * H,
+                           act, dtype, (cudaStream_t)stream);
   GatedIo io{};
   io.x = x;
-  io.Ws = reinterpret_cast<const float *>(static_cast<const char *>(Wspec) + spec_layout(N, Cin, H, dtype).simt_offset);
+  io.Ws = fp32_section(Wspec);
   io.out = h;
   io.T = T;
   io.Cin = Cin;
@@ -121,7 +161,7 @@ int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec
   const cudaStream_t s = (cudaStream_t)stream;
   int rc = check_shape(N, Cin, H, dtype);
   if (rc || (rc = check_call(T, N, Cin, H, act, path))) return rc;
-  if (path == EQLIN_PATH_TC) return set_error(EQLIN_ERR_UNSUPPORTED, "no tensor-core path for this layer");
+  if (path == EQLIN_PATH_TC && !tc_supported(N, Cin, H, dtype)) return set_error(EQLIN_ERR_UNSUPPORTED, kTcNeeds);
   if (!dx && !dW) return set_error(EQLIN_ERR_INVALID_ARG, "dx and dW are both null");
   if (!aligned(dW, 16)) return set_error(EQLIN_ERR_ALIGN, "dW must be 16-byte aligned");
   if (T == 0) {
@@ -132,34 +172,47 @@ int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec
   if (!x || !dh || !Wspec || (dx && !Wspec_adj)) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
   if (!aligned(x, 16) || !aligned(dh, 16) || !aligned(dx, 16) || !aligned(Wspec, 16) || !aligned(Wspec_adj, 16))
     return set_error(EQLIN_ERR_ALIGN, "x, dh, dx and the spectra must be 16-byte aligned");
+  if (path == EQLIN_PATH_TC && !aligned(dx, 32))
+    return set_error(EQLIN_ERR_ALIGN, "the tensor-core path needs dx 32-byte aligned");
   const BackwardParts p = backward_parts(T, N, Cin, H, dtype);
   if (!workspace) return set_error(EQLIN_ERR_INVALID_ARG, "null workspace");
   if (workspace_bytes < p.total)
     return set_error(EQLIN_ERR_SIZE, "workspace_bytes=%zu < required %zu", workspace_bytes, p.total);
   if (!aligned(workspace, 256)) return set_error(EQLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
   char *ws = static_cast<char *>(workspace);
-  GatedIo io{};
-  io.x = x;
-  io.Ws = reinterpret_cast<const float *>(static_cast<const char *>(Wspec) + spec_layout(N, Cin, H, dtype).simt_offset);
-  io.dh = dh;
-  io.out = ws + p.dp;
-  io.T = T;
-  io.Cin = Cin;
-  io.Cout = 2 * H;
-  if ((rc = launch_gated_simt(kEpiGates, io, N, act, dtype, s))) return rc;
-  if (dx) {
+  char *dp = ws + p.dp;
+  const bool tc = use_tc(T, N, Cin, H, dtype, path);
+  if (tc) {
+    rc = launch_gated_tc(kEpiGates, x, tc_section(Wspec, spec_layout(N, Cin, H, dtype)), dh, dp, T, Cin, 2 * H, act,
+                         dtype, s);
+  } else {
+    GatedIo io{};
+    io.x = x;
+    io.Ws = fp32_section(Wspec);
+    io.dh = dh;
+    io.out = dp;
+    io.T = T;
+    io.Cin = Cin;
+    io.Cout = 2 * H;
+    rc = launch_gated_simt(kEpiGates, io, N, act, dtype, s);
+  }
+  if (rc) return rc;
+  // (the wide kernel writes dx in 32-byte pieces)
+  if (dx && tc && (path == EQLIN_PATH_TC || aligned(dx, 32))) {
+    rc = launch_wide_tc(dp, tc_section(Wspec_adj, adjoint_layout(N, Cin, H, dtype)), dx, T, 2 * H, Cin, dtype, s);
+  } else if (dx) {
     GatedIo b{};
-    b.x = ws + p.dp;
-    b.Ws = reinterpret_cast<const float *>(static_cast<const char *>(Wspec_adj) +
-                                           adjoint_layout(N, Cin, H, dtype).simt_offset);
+    b.x = dp;
+    b.Ws = fp32_section(Wspec_adj);
     b.out = dx;
     b.T = T;
     b.Cin = 2 * H;
     b.Cout = Cin;
-    if ((rc = launch_gated_simt(kEpiLinear, b, N, EQLIN_ACT_NONE, dtype, s))) return rc;
+    rc = launch_gated_simt(kEpiLinear, b, N, EQLIN_ACT_NONE, dtype, s);
   }
+  if (rc) return rc;
   if (!dW) return EQLIN_OK;
-  return eqlin_cyclic_weight_grad_ex(x, ws + p.dp, dW, T, N, Cin, 2 * H, dtype, ws + p.part,
+  return eqlin_cyclic_weight_grad_ex(x, dp, dW, T, N, Cin, 2 * H, dtype, ws + p.part,
                                      workspace_bytes - p.part,
                                      path == EQLIN_PATH_SIMT ? EQLIN_PATH_SIMT : EQLIN_PATH_AUTO, stream);
 }

@@ -35,4 +35,23 @@ inline int launch_gated_simt(int epi, const GatedIo &io, int N, int act, int dty
                               : launch_gated_simt_t<__nv_bfloat16>(epi, io, N, act, s);
 }
 
+// Tensor-core form for C_8, bf16 and fp16 (spectral_tc.cu): kEpiGated or
+// kEpiGates of the layer Cin -> Cout = 2H (Cin and H multiples of 16, Cin <= 160)
+// from the packed weight stages Bpack (cyclic_tc_bytes), written by
+// launch_gated_tc_pack beside the fp32 spectrum Ws.
+int launch_gated_tc_pack(const void *W, int Cin, int Cout, int dtype, void *Ws, void *dst, cudaStream_t s);
+int launch_gated_tc(int epi, const void *x, const void *Bpack, const void *dh, void *out, int64_t T, int Cin,
+                    int Cout, int act, int dtype, cudaStream_t s);
+
+// C_8 layer with any number of input fields on tensor cores (gated_wide_tc.cu),
+// bf16 and fp16: y[T][F_out][8] from x[T][F_in][8], F_in a multiple of 16, F_out
+// of 8.  The pack (wide_tc_bytes) is W [F_out][F_in][8]'s, or with adjoint that
+// of V[o][i][m] = W[i][o][-m], W [F_in][F_out][8]; Ws: the fp32 spectrum beside it.
+bool wide_tc_supported(int N, int F_in, int F_out, int dtype);
+size_t wide_tc_bytes(int F_in, int F_out);
+int launch_wide_tc_pack(const void *W, int F_in, int F_out, bool adjoint, int dtype, void *Ws, void *dst,
+                        cudaStream_t s);
+int launch_wide_tc(const void *x, const void *pack, void *y, int64_t T, int F_in, int F_out, int dtype,
+                   cudaStream_t s);
+
 }  // namespace eqlin

@@ -43,6 +43,7 @@
 #include <mutex>
 
 #include "eqlin_internal.cuh"
+#include "gated_internal.cuh"
 #include "tc_primitives.cuh"
 #include "tc_host.h"
 #include "tc_transforms.cuh"
@@ -94,6 +95,11 @@ constexpr int kOutF32 = 8;
 // y [T][F_out][16] itself: y_g = ye_g + yo_g, y_{g+8} = ye_g - yo_g.
 constexpr int kCombine16 = 16;
 // negacyclic C_8 (the product modulo z^8 + 1): the odd half of a C_16 layer
+// The gated layer's epilogues (template parameter EPI: kEpiGated, kEpiGates of
+// gated_internal.cuh; kEpiLinear elsewhere): the activation, and TcArgs::y_even
+// is the gradient dh of the gated output.
+constexpr int kActSilu = 32;
+constexpr int kActGelu = 64;
 
 // warp roles
 constexpr int kThreads = 640;
@@ -571,6 +577,71 @@ __device__ __forceinline__ void d8_epilogue_group(uint32_t tb, int fg, int half,
   }
 }
 
+// One 8-column group (fg) of a gated layer's epilogue for one warp (cyclic C_8;
+// output fields 2j and 2j + 1 are field j's gate and value, so the two fields
+// of a thread's item are one pair).  kEpiGated writes h = act(gate) value, 16
+// bytes per item; kEpiGates reads dh there and writes the pair's gradients
+// (dh value act'(gate), dh act(gate)), 32 contiguous bytes.  The activations
+// are the paired forms of tc_transforms.cuh: exact to far below the operand
+// rounding of the products.  Not inlined, as neg16_epilogue_group.
+template <bool H, int EPI>
+__device__ __noinline__ void gated_epilogue_group(uint32_t tb, int fg, int half, int64_t tok0, int field_base,
+                                                  int64_t T, int F_out, uint8_t *ybase, const void *dh, int flags) {
+  using namespace tc;
+  const int hidden = F_out >> 1, j = (field_base + fg) >> 1;
+  uint4 dv[2];
+  if constexpr (EPI == kEpiGates) {   // loaded first: overlaps the TMEM loads
+#pragma unroll
+    for (int r8 = 0; r8 < 2; ++r8) {
+      const int64_t tok = tok0 + 8 * r8;
+      dv[r8] = __ldcs(reinterpret_cast<const uint4 *>(dh) + (tok < T ? tok : 0) * hidden + j);
+    }
+  }
+  uint32_t v[8][4];
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) tmem_ld_16x256b(tb + (uint32_t)(kk * half + fg), v[kk]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int r8 = 0; r8 < 2; ++r8) {   // token tok0 + 8 r8: gate in the x lanes, value in the y lanes
+    const int64_t tok = tok0 + 8 * r8;
+    float2 z[8], p[8];
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      z[group_coord(kModeCyclic8, kk)] =
+          make_float2(__uint_as_float(v[kk][2 * r8]), __uint_as_float(v[kk][2 * r8 + 1]));
+    inv_cyclic8(z, p);
+    if constexpr (EPI == kEpiGated) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 g = make_float2(p[2 * q].x, p[2 * q + 1].x), u = make_float2(p[2 * q].y, p[2 * q + 1].y);
+        const float2 a = flags & kActSilu ? silu2(g) : (flags & kActGelu ? gelu_erf2(g) : g);
+        const float2 h = mul2(a, u);
+        w[q] = pack_x2<H>(h.x, h.y);
+      }
+      if (tok < T)
+        reinterpret_cast<uint4 *>(ybase)[tok * hidden + j] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      const uint32_t dw[4] = {dv[r8].x, dv[r8].y, dv[r8].z, dv[r8].w};
+      uint32_t wg[4], wu[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 g = make_float2(p[2 * q].x, p[2 * q + 1].x), u = make_float2(p[2 * q].y, p[2 * q + 1].y);
+        const float2 d = unpack_x2<H>(dw[q]);
+        float2 a = g, s = make_float2(1.0f, 1.0f);
+        if (flags & kActSilu)
+          s = silu_slope2(g, a);
+        else if (flags & kActGelu)
+          s = gelu_slope2(g, a);
+        const float2 dg = mul2(mul2(d, u), s), du = mul2(d, a);
+        wg[q] = pack_x2<H>(dg.x, dg.y);
+        wu[q] = pack_x2<H>(du.x, du.y);
+      }
+      if (tok < T) st_global_v8(ybase + (tok * F_out + field_base + fg) * 16, wg, wu);
+    }
+  }
+}
+
 // Report a transformed block pair to the issuer (the leader CTA's a_full
 // barrier).  The leader's own warps arrive with a CTA-scope release, which is
 // all the issuer (in the same CTA) needs; the peer's warps need a cluster-scope
@@ -615,7 +686,7 @@ struct TcArgs {
   unsigned int epoch;   // this launch's fault epoch (next_launch_epoch)
 };
 
-template <int MODE, bool H>
+template <int MODE, bool H, int EPI = kEpiLinear>
 __global__ void __launch_bounds__(kThreads, 1)
     spectral8_tc_kernel(const __grid_constant__ CUtensorMap map_x,
                         const __grid_constant__ CUtensorMap map_b_full,
@@ -1087,6 +1158,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           neg16_epilogue_group(tb, fg, half, tok0, field_base, T, F_out, ybase, args.y_even);
           continue;
         }
+        if constexpr (EPI != kEpiLinear) {
+          gated_epilogue_group<H, EPI>(tb, fg, half, tok0, field_base, T, F_out, ybase, args.y_even, args.gelu);
+          continue;
+        }
         if constexpr (MODE == kModeCyclic4) {
           // four coordinate groups; a thread's two columns are the two C_4
           // fields of one output super-field, for token rows tr and tr + 8
@@ -1304,6 +1379,48 @@ __global__ void pack_b_kernel(const void *__restrict__ Wc, D8Blocks d8, int F_in
   }
 }
 
+// The same packing of a plain C_8 weight W[F_out][F_in][8] for the gated layer,
+// whole in one launch and in fp32 (a training step packs its weights anew each
+// time: one launch per chunk with 64-bit twiddles per element took 0.3 ms at 160
+// -> 864 fields): one thread per (output field, 8 input fields) computes their
+// half spectra and writes one 16-byte run per panel row, and the fp32 section
+// Ws[i][c][o] of the CUDA-core kernels.  Lanes walk the output fields.
+template <bool H>
+__global__ void __launch_bounds__(256)
+pack_c8_kernel(const uint4 *__restrict__ W, int F_in, int F_out, float *__restrict__ Ws, uint8_t *__restrict__ dst) {
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= (int64_t)F_out * (F_in / 8)) return;
+  const int o = (int)(idx % F_out), ib = (int)(idx / F_out);
+  uint32_t out[8][4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    float2 x[8], z[8];
+    const int i = 8 * ib + 2 * p;
+    unpack_x8_pair<H>(__ldg(W + (size_t)o * F_in + i), __ldg(W + (size_t)o * F_in + i + 1), x);
+    fwd_cyclic8(x, z);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float2 v = scl2(z[c], 0.125f);
+      Ws[((size_t)i * 8 + c) * F_out + o] = v.x;
+      Ws[((size_t)(i + 1) * 8 + c) * F_out + o] = v.y;
+      const float2 t = c == 0 || c == 7 ? v : scl2(v, 2.0f);   // the one-sided inverse's factor
+      out[c][p] = pack_x2<H>(t.x, t.y);
+    }
+  }
+  const int ch = o / kCoMax, co = chunk_fields(F_out, ch), hc = co / 2;
+  const int hh = (o - ch * kCoMax) / hc, r = (o - ch * kCoMax) % hc, kc = ib & 1;
+  uint8_t *stage = dst + stage_offset(kModeCyclic8, F_in, F_out, ch, ib >> 1, hh);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    // c = 0, 7: the real bins' panels; c = 2b - 1, 2b: Wr, Wi of bin b
+    const int k = c == 0 ? 0 : c == 7 ? 1 : 1 + (c + 1) / 2;
+    const int rows = panel_rows(kModeCyclic8, k, co);
+    const int row = k < 2 || c % 2 == 0 ? r : hc + r;
+    *reinterpret_cast<uint4 *>(stage + panel_offset(kModeCyclic8, k, co) + (kc * rows + row) * 16) =
+        make_uint4(out[c][0], out[c][1], out[c][2], out[c][3]);
+  }
+}
+
 template <int MODE, bool H = false, int WT = (H ? 1 : 0)>
 int launch_pack(const void *Wc, D8Blocks d8, int F_in, int F_out, int wsrc, void *dst,
                 cudaStream_t s, int split_cin = 0, int split_off = 0, int split_full = 0) {
@@ -1346,30 +1463,32 @@ int make_map_2d(CUtensorMap *m, const void *ptr, uint64_t inner, uint64_t outer,
   return EQLIN_OK;
 }
 
-struct DevCache {   // per mode, per operand type (bf16, fp16)
-  int max_clusters[4][2] = {};
-  bool attr_set[4][2] = {};
+struct DevCache {   // per mode and epilogue (rows 4, 5: the gated epilogues), per operand type (bf16, fp16)
+  int max_clusters[6][2] = {};
+  bool attr_set[6][2] = {};
 };
 std::mutex g_cache_mu;
 DevCache g_cache[64];
 
-template <int MODE, bool H = false>
+template <int MODE, bool H = false, int EPI = kEpiLinear>
 int launch_tc(const void *x, const void *Bpack, void *y, int64_t T, int F_in, int F_out, int gelu, int x_ld,
               cudaStream_t s, const void *y_even = nullptr) {
   if (T >= (int64_t)0x7fffff00LL) return set_error(EQLIN_ERR_UNSUPPORTED, "T too large");
-  if (((uintptr_t)y & 31u) != 0)
+  // (the gated output is written in 16-byte pieces)
+  if (((uintptr_t)y & (EPI == kEpiGated ? 15u : 31u)) != 0)
     return set_error(EQLIN_ERR_ALIGN, "tensor-core path needs y 32-byte aligned");
+  constexpr int kRow = EPI == kEpiLinear ? MODE : 3 + EPI;   // of the per-device cache
   const int ntiles = (int)((T + kTileTokens - 1) / kTileTokens);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
     return set_error(EQLIN_ERR_CUDA, "cudaGetDevice failed");
-  auto kern = spectral8_tc_kernel<MODE, H>;
+  auto kern = spectral8_tc_kernel<MODE, H, EPI>;
   const int smem_max = kSmemLimit;
   int maxc = 0;
   {
     std::lock_guard<std::mutex> lk(g_cache_mu);
     DevCache &dc = g_cache[dev];
-    if (!dc.attr_set[MODE][H]) {
+    if (!dc.attr_set[kRow][H]) {
       cudaError_t e =
           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
       if (e != cudaSuccess)
@@ -1390,10 +1509,10 @@ int launch_tc(const void *x, const void *Bpack, void *y, int64_t T, int F_in, in
       if (e != cudaSuccess || n <= 0)
         return set_error(EQLIN_ERR_CUDA, "cudaOccupancyMaxActiveClusters: %s (n=%d)",
                          cudaGetErrorString(e), n);
-      dc.max_clusters[MODE][H] = n;
-      dc.attr_set[MODE][H] = true;
+      dc.max_clusters[kRow][H] = n;
+      dc.attr_set[kRow][H] = true;
     }
-    maxc = dc.max_clusters[MODE][H];
+    maxc = dc.max_clusters[kRow][H];
   }
   CUtensorMap mx, mbf, mbl;
   // x rows are x_ld fields apart (F_in unless the layer reads a column slice)
@@ -1675,6 +1794,29 @@ int launch_cyclic_tc_f32(const void *x, const void *Bpack, void *y, int64_t T, i
     if (rc != EQLIN_OK) return rc;
   }
   return EQLIN_OK;
+}
+
+int launch_gated_tc_pack(const void *W, int Cin, int Cout, int dtype, void *Ws, void *dst, cudaStream_t s) {
+  const int64_t n = (int64_t)Cout * (Cin / 8);
+  const unsigned grid = (unsigned)((n + 255) / 256);
+  if (dtype == EQLIN_F16)
+    pack_c8_kernel<true><<<grid, 256, 0, s>>>(static_cast<const uint4 *>(W), Cin, Cout, static_cast<float *>(Ws),
+                                              static_cast<uint8_t *>(dst));
+  else
+    pack_c8_kernel<false><<<grid, 256, 0, s>>>(static_cast<const uint4 *>(W), Cin, Cout, static_cast<float *>(Ws),
+                                               static_cast<uint8_t *>(dst));
+  return check_launch("gated layer weight packing");
+}
+
+int launch_gated_tc(int epi, const void *x, const void *Bpack, const void *dh, void *out, int64_t T, int Cin,
+                    int Cout, int act, int dtype, cudaStream_t s) {
+  const int flags = act == EQLIN_ACT_SILU ? kActSilu : (act == EQLIN_ACT_GELU ? kActGelu : 0);
+  const bool f16 = dtype == EQLIN_F16;
+  if (epi == kEpiGated)
+    return f16 ? launch_tc<kModeCyclic8, true, kEpiGated>(x, Bpack, out, T, Cin, Cout, flags, Cin, s)
+               : launch_tc<kModeCyclic8, false, kEpiGated>(x, Bpack, out, T, Cin, Cout, flags, Cin, s);
+  return f16 ? launch_tc<kModeCyclic8, true, kEpiGates>(x, Bpack, out, T, Cin, Cout, flags, Cin, s, dh)
+             : launch_tc<kModeCyclic8, false, kEpiGates>(x, Bpack, out, T, Cin, Cout, flags, Cin, s, dh);
 }
 
 bool cyclic_tc_f16_supported(int N, int Cin, int Cout, int dtype) {

@@ -245,6 +245,52 @@ __host__ __device__ __forceinline__ float2 gelu_tanh2(float2 v) {
   return fma2(h, t, h);
 }
 
+// SiLU(v) = v s, s = 1 / (1 + e^-v), and its slope s (1 + v (1 - s)), with the
+// fast exponential and quotient (relative error below 1e-6 where the result is
+// not negligible); `a` receives the value.
+__host__ __device__ __forceinline__ float2 sigmoid2(float2 v) {
+#ifdef __CUDA_ARCH__
+  return make_float2(__fdividef(1.0f, 1.0f + __expf(-v.x)), __fdividef(1.0f, 1.0f + __expf(-v.y)));
+#else
+  return make_float2(1.0f / (1.0f + expf(-v.x)), 1.0f / (1.0f + expf(-v.y)));
+#endif
+}
+__host__ __device__ __forceinline__ float2 silu2(float2 v) { return mul2(v, sigmoid2(v)); }
+__host__ __device__ __forceinline__ float2 silu_slope2(float2 v, float2 &a) {
+  const float2 s = sigmoid2(v);
+  const float2 one = make_float2(1.0f, 1.0f);
+  a = mul2(v, s);
+  return mul2(s, fma2(v, sub2(one, s), one));
+}
+
+// GELU's value (in `a`, as gelu_erf2) and slope Phi(v) + v phi(v), phi the
+// normal density: with h as there, v Phi(v) = a and Phi(v) = 1 - r / 2 or r / 2.
+__host__ __device__ __forceinline__ float2 gelu_slope2(float2 v, float2 &a) {
+  const float2 x = scl2(make_float2(fabsf(v.x), fabsf(v.y)), 0.70710678118654752f);
+  float2 p = make_float2(0.0000430638f, 0.0000430638f);
+  p = fma2(p, x, make_float2(0.0002765672f, 0.0002765672f));
+  p = fma2(p, x, make_float2(0.0001520143f, 0.0001520143f));
+  p = fma2(p, x, make_float2(0.0092705272f, 0.0092705272f));
+  p = fma2(p, x, make_float2(0.0422820123f, 0.0422820123f));
+  p = fma2(p, x, make_float2(0.0705230784f, 0.0705230784f));
+  p = fma2(p, x, make_float2(1.0f, 1.0f));
+  p = mul2(p, p);
+  p = mul2(p, p);
+  p = mul2(p, p);
+  p = mul2(p, p);
+  const float2 e = scl2(mul2(v, v), -0.5f);
+#ifdef __CUDA_ARCH__
+  const float2 r = make_float2(__fdividef(0.5f, p.x), __fdividef(0.5f, p.y));
+  const float2 d = make_float2(__expf(e.x), __expf(e.y));
+#else
+  const float2 r = make_float2(0.5f / p.x, 0.5f / p.y);
+  const float2 d = make_float2(expf(e.x), expf(e.y));
+#endif
+  const float2 phi = make_float2(v.x >= 0.0f ? 1.0f - r.x : r.x, v.y >= 0.0f ? 1.0f - r.y : r.y);
+  a = mul2(v, phi);
+  return fma2(scl2(v, 0.39894228040143268f), d, phi);
+}
+
 // p4 (C_4) on the fused kernel: a 16-byte chunk holds two C_4 fields (a
 // "super-field" of 8 slots).  The 4-point DFT has entries 0, +-1, +-i, so
 // both transforms are additions.  Coordinates per C_4 field: [Re X0, Re X1,
@@ -316,6 +362,12 @@ __device__ __forceinline__ void unpack_x8_pair(const uint4 &a, const uint4 &b, f
     unpack_f16x8_pair(a, b, f);
   else
     unpack_bf16x8_pair(a, b, f);
+}
+// A packed pair of either type to fp32.
+template <bool H>
+__device__ __forceinline__ float2 unpack_x2(uint32_t w) {
+  if (H) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 template <bool H>
 __device__ __forceinline__ uint32_t pack_x2(float lo, float hi) {

@@ -114,6 +114,45 @@ def test_cuda_cores(T, C, H, N, act, dtype):
     run(T, C, H, N, dtype, act, path=eq.PATH_SIMT)
 
 
+# tensor cores: ragged tiles, one 32-field chunk or several, output groups of dx with padding (Cin = 16, 48, ..),
+# several tiles per pair of CTAs
+TC = [
+    (33, 16, 16, "silu"), (64, 32, 48, "gelu"), (127, 48, 16, "none"), (128, 80, 64, "silu"), (129, 112, 80, "gelu"),
+    (300, 160, 432, "silu"), (1000, 144, 96, "gelu"), (3 * 74 * 128 + 77, 32, 32, "silu"),
+    (2 * 74 * 128 + 1, 160, 48, "silu"), (20000, 96, 160, "gelu"),
+]
+
+
+@pytest.mark.parametrize("T,C,H,act", TC)
+def test_tensor_cores(T, C, H, act):
+    assert eq.cyclic_gated_auto_path(8, C, H, BF16) == eq.PATH_TC
+    run(T, C, H, 8, BF16, act, halves=(2, 2.5, 2.5))
+
+
+@pytest.mark.parametrize("T,C,H,act", TC[:7] + [(1, 32, 16, "silu")])
+def test_tensor_cores_when_asked_for(T, C, H, act):
+    """fp16, and bf16 for a handful of tokens."""
+    run(T, C, H, 8, F16, act, path=eq.PATH_TC, halves=(2, 2.5, 2.5))
+    run(T % 32 + 1, C, H, 8, BF16, act, path=eq.PATH_TC, halves=(2, 2.5, 2.5))
+
+
+def test_outputs_at_odd_addresses():
+    """h and dx 16 bytes off a 32-byte boundary: written whole, or refused when the tensor cores are asked for."""
+    T, C, H = 200, 32, 48
+    x, W, dh = tensors(T, C, H, 8, BF16, 9)
+    spec, adj = eq.cyclic_gated_weight_spectrum(W), eq.cyclic_gated_weight_spectrum_adjoint(W)
+    rh, rdx, rdW = reference(x, W, "silu", dh)
+    h = torch.empty(T * H * 8 + 8, dtype=BF16, device="cuda")[8:].view(T, H, 8)
+    dx = torch.empty(T * C * 8 + 8, dtype=BF16, device="cuda")[8:].view(T, C, 8)
+    dW = torch.empty(H * 2 * C * 8 + 8, dtype=BF16, device="cuda")[8:].view(H, 2, C, 8)
+    near(eq.cyclic_gated_forward(x, spec, H, h=h), rh, 2)
+    eq.cyclic_gated_backward(x, dh, spec, adj, dx=dx, dW=dW)
+    near(dx, rdx, 2.5)
+    near(dW, rdW, 2.5)
+    with pytest.raises(eq.EqlinError):
+        eq.cyclic_gated_backward(x, dh, spec, adj, dx=dx, path=eq.PATH_TC)
+
+
 def test_no_tokens():
     x, W, dh = tensors(0, 16, 8, 8, F32, 0)
     spec, adj = eq.cyclic_gated_weight_spectrum(W), eq.cyclic_gated_weight_spectrum_adjoint(W)
