@@ -79,7 +79,8 @@ _SIGS = {
     "eqlin_cyclic_gated_adjoint_bytes": (_sz, [_i, _i, _i, _i]),
     "eqlin_cyclic_gated_weight_spectrum_adjoint": (_i, [_vp, _i, _i, _i, _i, _vp, _sz, _vp]),
     "eqlin_cyclic_gated_auto_path": (_i, [_i, _i, _i, _i]),
-    "eqlin_cyclic_gated_forward": (_i, [_vp, _vp, _vp, _i64, _i, _i, _i, _i, _i, _i, _vp]),
+    "eqlin_cyclic_gated_forward_workspace_bytes": (_sz, [_i64, _i, _i, _i, _i]),
+    "eqlin_cyclic_gated_forward": (_i, [_vp, _vp, _vp, _i64, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
     "eqlin_cyclic_gated_backward_workspace_bytes": (_sz, [_i64, _i, _i, _i, _i]),
     "eqlin_cyclic_gated_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _i, _i, _vp, _sz,
                                          _vp]),
@@ -410,23 +411,32 @@ def d8_fourier_mlp(z: torch.Tensor, W1pack: torch.Tensor, W2pack: torch.Tensor, 
 # ------------------------------------------------------------------ gated feed-forward
 
 
-def _run(where: str, device: torch.device, *args):
-    """Call the entry point `where` with the tensors' device current, on that
-    device's current stream."""
-    fn = getattr(_lib, where)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream_ptr(device))
+def _run(fn, where: str, device: torch.device, *args):
+    """Call an entry point with the tensors' device current, on that device's
+    current stream."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, _stream_ptr(device))
-    _check(rc, where)
+            rc = fn(*args, _raw_stream(index))
+    if rc != EQLIN_OK:
+        raise EqlinError(rc, where)
 
 
-def _on(device: torch.device, t: torch.Tensor, name: str):
-    """The address of t, which must be contiguous and on `device`."""
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _on(device: torch.device, t: torch.Tensor, name: str) -> int:
+    """The address of t, which must be contiguous and on `device` (a GPU)."""
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return _dev_ptr(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _given(t: torch.Tensor | None, shape, dtype: torch.dtype, device: torch.device, name: str) -> torch.Tensor:
@@ -469,7 +479,7 @@ def cyclic_gated_weight_spectrum(W: torch.Tensor, out: torch.Tensor | None = Non
         raise EqlinError(EQLIN_ERR_UNSUPPORTED, "eqlin_cyclic_gated_spectrum_bytes")
     if out is None:
         out = torch.empty(need, dtype=torch.uint8, device=W.device)
-    _run("eqlin_cyclic_gated_weight_spectrum", W.device, _dev_ptr(W, "W"), N, Cin, H, dtype_code(W.dtype),
+    _run(_lib.eqlin_cyclic_gated_weight_spectrum, "eqlin_cyclic_gated_weight_spectrum", W.device, _on(W.device, W, "W"), N, Cin, H, dtype_code(W.dtype),
          _on(W.device, out, "Wspec"), out.numel())
     return out
 
@@ -482,7 +492,7 @@ def cyclic_gated_weight_spectrum_adjoint(W: torch.Tensor, out: torch.Tensor | No
         raise EqlinError(EQLIN_ERR_UNSUPPORTED, "eqlin_cyclic_gated_adjoint_bytes")
     if out is None:
         out = torch.empty(need, dtype=torch.uint8, device=W.device)
-    _run("eqlin_cyclic_gated_weight_spectrum_adjoint", W.device, _dev_ptr(W, "W"), N, Cin, H,
+    _run(_lib.eqlin_cyclic_gated_weight_spectrum_adjoint, "eqlin_cyclic_gated_weight_spectrum_adjoint", W.device, _on(W.device, W, "W"), N, Cin, H,
          dtype_code(W.dtype), _on(W.device, out, "Wspec_adj"), out.numel())
     return out
 
@@ -494,15 +504,24 @@ def _spectrum_ptr(device: torch.device, spec: torch.Tensor, need: int, name: str
 
 
 def cyclic_gated_forward(x: torch.Tensor, Wspec: torch.Tensor, H: int, act: int = ACT_SILU,
-                         h: torch.Tensor | None = None, path: int = PATH_AUTO) -> torch.Tensor:
+                         h: torch.Tensor | None = None, path: int = PATH_AUTO,
+                         workspace: torch.Tensor | None = None) -> torch.Tensor:
     """x [T, Cin, N] (device) -> h [T, H, N] = act(gate) * value, gate and value
-    the two cyclic layers of W (see cyclic_gated_weight_spectrum)."""
+    the two cyclic layers of W (see cyclic_gated_weight_spectrum).  The
+    workspace (a device byte tensor of cyclic_gated_forward_workspace_bytes) is
+    allocated here when not given and needed."""
     T, Cin, N = x.shape
     dt, dev = dtype_code(x.dtype), x.device
     h = _given(h, (T, H, N), x.dtype, dev, "h")
     spec = _spectrum_ptr(dev, Wspec, int(_lib.eqlin_cyclic_gated_spectrum_bytes(N, Cin, H, dt)), "Wspec")
-    _run("eqlin_cyclic_gated_forward", dev, _dev_ptr(x, "x"), spec, _on(dev, h, "h"), T, N, Cin, H, act, dt, path)
+    ws, ws_bytes, _ = _scratch(workspace, int(_lib.eqlin_cyclic_gated_forward_workspace_bytes(T, N, Cin, H, dt)), dev)
+    _run(_lib.eqlin_cyclic_gated_forward, "eqlin_cyclic_gated_forward", dev, _on(dev, x, "x"), spec, _on(dev, h, "h"), T, N, Cin, H, act, dt, path,
+         ws, ws_bytes)
     return h
+
+
+def cyclic_gated_forward_workspace_bytes(T: int, N: int, Cin: int, H: int, dtype: torch.dtype) -> int:
+    return int(_lib.eqlin_cyclic_gated_forward_workspace_bytes(T, N, Cin, H, dtype_code(dtype)))
 
 
 def cyclic_gated_backward_workspace_bytes(T: int, N: int, Cin: int, H: int, dtype: torch.dtype) -> int:
@@ -525,7 +544,7 @@ def cyclic_gated_backward(x: torch.Tensor, dh: torch.Tensor, Wspec: torch.Tensor
     spec = _spectrum_ptr(dev, Wspec, int(_lib.eqlin_cyclic_gated_spectrum_bytes(N, Cin, H, dt)), "Wspec")
     adj = _spectrum_ptr(dev, Wspec_adj, int(_lib.eqlin_cyclic_gated_adjoint_bytes(N, Cin, H, dt)), "Wspec_adj")
     ws, ws_bytes, _ = _scratch(workspace, cyclic_gated_backward_workspace_bytes(T, N, Cin, H, x.dtype), dev)
-    _run("eqlin_cyclic_gated_backward", dev, _dev_ptr(x, "x"), _on(dev, dh, "dh"), spec, adj, _on(dev, dx, "dx"),
+    _run(_lib.eqlin_cyclic_gated_backward, "eqlin_cyclic_gated_backward", dev, _on(dev, x, "x"), _on(dev, dh, "dh"), spec, adj, _on(dev, dx, "dx"),
          _on(dev, dW, "dW"), T, N, Cin, H, act, dt, path, ws, ws_bytes)
     return dx, dW
 
@@ -565,7 +584,7 @@ def group_norm(x: torch.Tensor, groups: int, gamma: torch.Tensor | None = None, 
     mean = _given(mean, (B, groups), torch.float32, dev, "mean")
     rstd = _given(rstd, (B, groups), torch.float32, dev, "rstd")
     ws, ws_bytes, _ = _scratch(workspace, int(_lib.eqlin_group_norm_workspace_bytes(B, S, F, N, groups, dt)), dev)
-    _run("eqlin_group_norm", dev, _dev_ptr(x, "x"), _affine_ptr(gamma, F, x, "gamma"),
+    _run(_lib.eqlin_group_norm, "eqlin_group_norm", dev, _on(dev, x, "x"), _affine_ptr(gamma, F, x, "gamma"),
          _affine_ptr(beta, F, x, "beta"), _on(dev, y, "y"), _on(dev, mean, "mean"), _on(dev, rstd, "rstd"),
          B, S, F, N, groups, eps, act, dt, ws, ws_bytes)
     return y, mean, rstd
@@ -588,7 +607,7 @@ def group_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
     dbeta = torch.empty_like(beta) if beta is not None else None
     ws, ws_bytes, _ = _scratch(
         workspace, int(_lib.eqlin_group_norm_backward_workspace_bytes(B, S, F, N, groups, dt)), dev)
-    _run("eqlin_group_norm_backward", dev, _dev_ptr(x, "x"), _on(dev, dy, "dy"), _on(dev, mean, "mean"),
+    _run(_lib.eqlin_group_norm_backward, "eqlin_group_norm_backward", dev, _on(dev, x, "x"), _on(dev, dy, "dy"), _on(dev, mean, "mean"),
          _on(dev, rstd, "rstd"), _affine_ptr(gamma, F, x, "gamma"), _affine_ptr(beta, F, x, "beta"),
          _on(dev, dx, "dx"), _affine_ptr(dgamma, F, x, "dgamma"), _affine_ptr(dbeta, F, x, "dbeta"),
          B, S, F, N, groups, act, dt, ws, ws_bytes)

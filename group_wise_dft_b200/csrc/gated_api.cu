@@ -13,7 +13,7 @@ int check_shape(int N, int Cin, int H, int dtype) {
   return check_cyclic_shape(N, Cin, 2 * H, dtype);
 }
 
-const char *kTcNeeds = "the gated layer's tensor-core path needs bf16 or fp16, N=8, Cin%%16==0 (16..160) and H%%16==0";
+const char *kTcNeeds = "the gated layer's tensor-core path needs bf16 or fp16, Cin >= 16 and H >= 8";
 
 int check_call(int64_t T, int N, int Cin, int H, int act, int path) {
   if (T < 0) return set_error(EQLIN_ERR_INVALID_ARG, "T=%lld < 0", (long long)T);
@@ -42,33 +42,56 @@ SpecLayout layout(int N, int F_in, int F_out, size_t tc_bytes) {
   L.total = L.tc_offset + tc_bytes;
   return L;
 }
-bool tc_supported(int N, int Cin, int H, int dtype) {
-  return cyclic_tc_supported(N, Cin, 2 * H, dtype) || cyclic_tc_f16_supported(N, Cin, 2 * H, dtype);
+// The fused C_8 kernel where its shapes fit, the two-pass products for the rest
+// of the 16-bit layers.
+#ifndef EQLIN_GEMM8
+#define EQLIN_GEMM8 0
+#endif
+#ifndef EQLIN_GEMMDX
+#define EQLIN_GEMMDX 0
+#endif
+enum Tc { kTcNone, kTcFused, kTcGemm };
+Tc tc_kind(int N, int Cin, int H, int dtype) {
+  if (!EQLIN_GEMM8 && (cyclic_tc_supported(N, Cin, 2 * H, dtype) || cyclic_tc_f16_supported(N, Cin, 2 * H, dtype))) return kTcFused;
+  return gemm_tc_supported(N, Cin, 2 * H, dtype) && gemm_tc_supported(N, 2 * H, Cin, dtype) ? kTcGemm : kTcNone;
 }
 SpecLayout spec_layout(int N, int Cin, int H, int dtype) {
-  return layout(N, Cin, 2 * H, tc_supported(N, Cin, H, dtype) ? cyclic_tc_bytes(N, Cin, 2 * H) : 0);
+  const Tc k = tc_kind(N, Cin, H, dtype);
+  return layout(N, Cin, 2 * H, k == kTcFused ? cyclic_tc_bytes(N, Cin, 2 * H) : k == kTcGemm ? gemm_tc_bytes(N, Cin, 2 * H) : 0);
 }
 SpecLayout adjoint_layout(int N, int Cin, int H, int dtype) {
-  return layout(N, 2 * H, Cin, tc_supported(N, Cin, H, dtype) ? wide_tc_bytes(2 * H, Cin) : 0);
+  const Tc k = tc_kind(N, Cin, H, dtype);
+  return layout(N, 2 * H, Cin, k == kTcFused && !EQLIN_GEMMDX ? wide_tc_bytes(2 * H, Cin) : k != kTcNone ? gemm_tc_bytes(N, 2 * H, Cin) : 0);
 }
 const float *fp32_section(const void *spec) { return static_cast<const float *>(spec); }
 const void *tc_section(const void *spec, const SpecLayout &L) { return static_cast<const char *>(spec) + L.tc_offset; }
 
 // Few tokens go to the CUDA cores: they spread the weights' reading over the
-// whole GPU, where one tile of the tensor-core kernel would keep a single pair
+// whole GPU, where one tile of the tensor-core kernels would keep a single pair
 // of SMs busy.
 constexpr int64_t kTcTokensLeast = 33;
-bool use_tc(int64_t T, int N, int Cin, int H, int dtype, int path) {
-  if (!tc_supported(N, Cin, H, dtype) || path == EQLIN_PATH_SIMT) return false;
-  return path == EQLIN_PATH_TC || (dtype == EQLIN_BF16 && T >= kTcTokensLeast);
+Tc tc_for(int64_t T, int N, int Cin, int H, int dtype, int path) {
+  const Tc k = tc_kind(N, Cin, H, dtype);
+  if (path == EQLIN_PATH_SIMT || !gemm_tc_tokens_ok(T, N, Cin > 2 * H ? Cin : 2 * H)) return kTcNone;
+  if (path == EQLIN_PATH_AUTO && (dtype != EQLIN_BF16 || T < kTcTokensLeast)) return kTcNone;
+  return k;
+}
+size_t forward_workspace(int64_t T, int N, int Cin, int H, int dtype) {
+  return tc_kind(N, Cin, H, dtype) == kTcGemm ? round256(gemm_tc_spectra_bytes(T, N, Cin)) : 0;
 }
 
 struct BackwardParts {
-  size_t dp, part, total;   // dp [T][2H][N] `dtype`; the weight gradient's partials
+  size_t dp, spec, part, total;   // dp [T][2H][N] `dtype`; spectra of x, then of dp; the weight gradient's partials
 };
 BackwardParts backward_parts(int64_t T, int N, int Cin, int H, int dtype) {
   BackwardParts p{};
-  p.part = round256((size_t)T * 2 * H * N * elem_size(dtype));
+  p.spec = round256((size_t)T * 2 * H * N * elem_size(dtype));
+  p.part = p.spec;
+  const Tc k = tc_kind(N, Cin, H, dtype);
+  if (k == kTcGemm || (k == kTcFused && EQLIN_GEMMDX)) {
+    const size_t a = gemm_tc_spectra_bytes(T, N, Cin), b = gemm_tc_spectra_bytes(T, N, 2 * H);
+    p.part += round256(a > b ? a : b);
+  }
   p.total = p.part + round256(eqlin_cyclic_weight_grad_workspace_bytes(T, N, Cin, 2 * H, dtype));
   return p;
 }
@@ -84,6 +107,10 @@ int weight_spectrum(const void *W, int N, int Cin, int H, int dtype, bool adjoin
   if (bytes < L.total) return set_error(EQLIN_ERR_SIZE, "spectrum buffer of %zu bytes < required %zu", bytes, L.total);
   if (L.tc_bytes) {
     char *tc = static_cast<char *>(out) + L.tc_offset;
+    const Tc k = tc_kind(N, Cin, H, dtype);
+    if (k == kTcGemm || (adjoint && EQLIN_GEMMDX))
+      return adjoint ? launch_gemm_tc_pack(W, N, 2 * H, Cin, true, dtype, out, tc, s)
+                     : launch_gemm_tc_pack(W, N, Cin, 2 * H, false, dtype, out, tc, s);
     return adjoint ? launch_wide_tc_pack(W, 2 * H, Cin, true, dtype, out, tc, s)
                    : launch_gated_tc_pack(W, Cin, 2 * H, dtype, out, tc, s);
   }
@@ -121,22 +148,42 @@ int eqlin_cyclic_gated_weight_spectrum_adjoint(const void *W, int N, int Cin, in
 
 int eqlin_cyclic_gated_auto_path(int N, int Cin, int H, int dtype) {
   if (check_shape(N, Cin, H, dtype) != EQLIN_OK) return -1;
-  return tc_supported(N, Cin, H, dtype) && dtype == EQLIN_BF16 ? EQLIN_PATH_TC : EQLIN_PATH_SIMT;
+  return tc_kind(N, Cin, H, dtype) != kTcNone && dtype == EQLIN_BF16 ? EQLIN_PATH_TC : EQLIN_PATH_SIMT;
+}
+
+size_t eqlin_cyclic_gated_forward_workspace_bytes(int64_t T, int N, int Cin, int H, int dtype) {
+  if (check_shape(N, Cin, H, dtype) != EQLIN_OK || T <= 0 ||
+      check_call(T, N, Cin, H, EQLIN_ACT_NONE, EQLIN_PATH_AUTO) != EQLIN_OK)
+    return 0;
+  return forward_workspace(T, N, Cin, H, dtype);
 }
 
 int eqlin_cyclic_gated_forward(const void *x, const void *Wspec, void *h, int64_t T, int N, int Cin, int H, int act,
-                               int dtype, int path, eqlin_stream_t stream) {
+                               int dtype, int path, void *workspace, size_t workspace_bytes, eqlin_stream_t stream) {
   clear_error();
   int rc = check_shape(N, Cin, H, dtype);
   if (rc || (rc = check_call(T, N, Cin, H, act, path))) return rc;
-  if (path == EQLIN_PATH_TC && !tc_supported(N, Cin, H, dtype)) return set_error(EQLIN_ERR_UNSUPPORTED, kTcNeeds);
+  if (path == EQLIN_PATH_TC && tc_for(T, N, Cin, H, dtype, path) == kTcNone)
+    return set_error(EQLIN_ERR_UNSUPPORTED, "%s", kTcNeeds);
   if (T == 0) return EQLIN_OK;
   if (!x || !Wspec || !h) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
   if (!aligned(x, 16) || !aligned(h, 16) || !aligned(Wspec, 16))
     return set_error(EQLIN_ERR_ALIGN, "x, h and Wspec must be 16-byte aligned");
-  if (use_tc(T, N, Cin, H, dtype, path))
-    return launch_gated_tc(kEpiGated, x, tc_section(Wspec, spec_layout(N, Cin, H, dtype)), nullptr, h, T, Cin, 2 * H,
-                           act, dtype, (cudaStream_t)stream);
+  const cudaStream_t s = (cudaStream_t)stream;
+  Tc k = tc_for(T, N, Cin, H, dtype, path);
+  if (k == kTcGemm) {
+    const size_t need = forward_workspace(T, N, Cin, H, dtype);
+    const bool ok = workspace && workspace_bytes >= need && aligned(workspace, 256);
+    if (!ok && path == EQLIN_PATH_TC)
+      return set_error(EQLIN_ERR_SIZE, "this tensor-core path needs a 256-byte aligned workspace of %zu bytes", need);
+    if (!ok) k = kTcNone;
+  }
+  const void *pack = tc_section(Wspec, spec_layout(N, Cin, H, dtype));
+  if (k == kTcFused) return launch_gated_tc(kEpiGated, x, pack, nullptr, h, T, Cin, 2 * H, act, dtype, s);
+  if (k == kTcGemm) {
+    if ((rc = launch_gemm_tc_spectra(x, workspace, T, N, Cin, dtype, s))) return rc;
+    return launch_gemm_tc(kEpiGated, workspace, pack, nullptr, h, T, N, Cin, 2 * H, act, dtype, s);
+  }
   GatedIo io{};
   io.x = x;
   io.Ws = fp32_section(Wspec);
@@ -144,7 +191,7 @@ int eqlin_cyclic_gated_forward(const void *x, const void *Wspec, void *h, int64_
   io.T = T;
   io.Cin = Cin;
   io.Cout = 2 * H;
-  return launch_gated_simt(kEpiGated, io, N, act, dtype, (cudaStream_t)stream);
+  return launch_gated_simt(kEpiGated, io, N, act, dtype, s);
 }
 
 size_t eqlin_cyclic_gated_backward_workspace_bytes(int64_t T, int N, int Cin, int H, int dtype) {
@@ -161,7 +208,8 @@ int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec
   const cudaStream_t s = (cudaStream_t)stream;
   int rc = check_shape(N, Cin, H, dtype);
   if (rc || (rc = check_call(T, N, Cin, H, act, path))) return rc;
-  if (path == EQLIN_PATH_TC && !tc_supported(N, Cin, H, dtype)) return set_error(EQLIN_ERR_UNSUPPORTED, kTcNeeds);
+  if (path == EQLIN_PATH_TC && tc_for(T, N, Cin, H, dtype, path) == kTcNone)
+    return set_error(EQLIN_ERR_UNSUPPORTED, "%s", kTcNeeds);
   if (!dx && !dW) return set_error(EQLIN_ERR_INVALID_ARG, "dx and dW are both null");
   if (!aligned(dW, 16)) return set_error(EQLIN_ERR_ALIGN, "dW must be 16-byte aligned");
   if (T == 0) {
@@ -172,7 +220,7 @@ int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec
   if (!x || !dh || !Wspec || (dx && !Wspec_adj)) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
   if (!aligned(x, 16) || !aligned(dh, 16) || !aligned(dx, 16) || !aligned(Wspec, 16) || !aligned(Wspec_adj, 16))
     return set_error(EQLIN_ERR_ALIGN, "x, dh, dx and the spectra must be 16-byte aligned");
-  if (path == EQLIN_PATH_TC && !aligned(dx, 32))
+  if (path == EQLIN_PATH_TC && tc_kind(N, Cin, H, dtype) == kTcFused && !aligned(dx, 32))
     return set_error(EQLIN_ERR_ALIGN, "the tensor-core path needs dx 32-byte aligned");
   const BackwardParts p = backward_parts(T, N, Cin, H, dtype);
   if (!workspace) return set_error(EQLIN_ERR_INVALID_ARG, "null workspace");
@@ -181,10 +229,14 @@ int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec
   if (!aligned(workspace, 256)) return set_error(EQLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
   char *ws = static_cast<char *>(workspace);
   char *dp = ws + p.dp;
-  const bool tc = use_tc(T, N, Cin, H, dtype, path);
-  if (tc) {
-    rc = launch_gated_tc(kEpiGates, x, tc_section(Wspec, spec_layout(N, Cin, H, dtype)), dh, dp, T, Cin, 2 * H, act,
-                         dtype, s);
+  void *S = ws + p.spec;
+  const Tc k = tc_for(T, N, Cin, H, dtype, path);
+  const void *pack = tc_section(Wspec, spec_layout(N, Cin, H, dtype));
+  if (k == kTcFused) {
+    rc = launch_gated_tc(kEpiGates, x, pack, dh, dp, T, Cin, 2 * H, act, dtype, s);
+  } else if (k == kTcGemm) {
+    rc = launch_gemm_tc_spectra(x, S, T, N, Cin, dtype, s);
+    if (!rc) rc = launch_gemm_tc(kEpiGates, S, pack, dh, dp, T, N, Cin, 2 * H, act, dtype, s);
   } else {
     GatedIo io{};
     io.x = x;
@@ -197,18 +249,23 @@ int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec
     rc = launch_gated_simt(kEpiGates, io, N, act, dtype, s);
   }
   if (rc) return rc;
-  // (the wide kernel writes dx in 32-byte pieces)
-  if (dx && tc && (path == EQLIN_PATH_TC || aligned(dx, 32))) {
-    rc = launch_wide_tc(dp, tc_section(Wspec_adj, adjoint_layout(N, Cin, H, dtype)), dx, T, 2 * H, Cin, dtype, s);
-  } else if (dx) {
-    GatedIo b{};
-    b.x = dp;
-    b.Ws = fp32_section(Wspec_adj);
-    b.out = dx;
-    b.T = T;
-    b.Cin = 2 * H;
-    b.Cout = Cin;
-    rc = launch_gated_simt(kEpiLinear, b, N, EQLIN_ACT_NONE, dtype, s);
+  if (dx) {
+    const void *adj = tc_section(Wspec_adj, adjoint_layout(N, Cin, H, dtype));
+    if (k == kTcGemm || (k == kTcFused && EQLIN_GEMMDX)) {
+      rc = launch_gemm_tc_spectra(dp, S, T, N, 2 * H, dtype, s);
+      if (!rc) rc = launch_gemm_tc(kEpiLinear, S, adj, nullptr, dx, T, N, 2 * H, Cin, EQLIN_ACT_NONE, dtype, s);
+    } else if (k == kTcFused && (path == EQLIN_PATH_TC || aligned(dx, 32))) {   // dx in 32-byte pieces
+      rc = launch_wide_tc(dp, adj, dx, T, 2 * H, Cin, dtype, s);
+    } else {
+      GatedIo b{};
+      b.x = dp;
+      b.Ws = fp32_section(Wspec_adj);
+      b.out = dx;
+      b.T = T;
+      b.Cin = 2 * H;
+      b.Cout = Cin;
+      rc = launch_gated_simt(kEpiLinear, b, N, EQLIN_ACT_NONE, dtype, s);
+    }
   }
   if (rc) return rc;
   if (!dW) return EQLIN_OK;

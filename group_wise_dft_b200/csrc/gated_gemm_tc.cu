@@ -1,0 +1,641 @@
+// Cyclic layers of any N on tcgen05 tensor cores, for the gated layer: the
+// projections with their gate (or the gate's gradients) as the epilogue, and the
+// wide data gradient.  bf16 or fp16 operands, fp32 accumulation.
+//
+// Two passes.  A pre-pass writes the half spectra of x, rounded to the operand
+// type, as N matrices S[c][t][i] (coordinate c of DftTables' order): reads and
+// writes x once.  The product kernel is then a plain streaming GEMM per bin whose
+// accumulators, all N coordinates of 128 tokens x up to 128 output fields, stay
+// in TMEM until the inverse DFT, which needs every bin of a field at once:
+//     real bins:    Y += X W,      complex bins: [Im|Re] Y += Re X . [Wi; Wr],
+//     Im Y += Im X . Wr,  Re Y -= Im X . Wi.
+//
+// CTA pair (cluster of 2, cta_group::2, M = 128: 64 tokens per CTA); a work unit
+// is (token tile, group of co output fields), N co / 2 <= 512 TMEM columns.  Its
+// stages are (64 input fields, one complex bin or the two real ones): A two
+// 64 x 64 boxes of S (16 KB per CTA), B co rows of the packed weights (128 co
+// bytes per CTA), both by TMA with the 128-byte swizzle, all signalling the
+// leader's barrier of the ring slot.  Warps: producer (one thread), MMA issuer
+// (leader), 12 epilogue warps (TMEM -> inverse DFT -> activation and product ->
+// global).  Where two units' accumulators fit TMEM, one unit's epilogue runs
+// under the next one's products.
+// The spectra cost a pass over x that the fused C_8 kernel does not have, but
+// nothing is transformed twice and no transform sits between a load and its MMA:
+// what paces the kernel is the operands' way from L2 (A and B of a stage serve 64
+// x co outputs only).  Every wait is bounded, as in the other kernels.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "dft_pairs.cuh"
+#include "gated_internal.cuh"
+#include "tc_host.h"
+#include "tc_primitives.cuh"
+
+namespace eqlin {
+namespace {
+
+constexpr int kProd = 0;          // TMA producer; TMEM allocation
+constexpr int kMma = 1;           // MMA issuer (leader)
+constexpr int kEpi0 = 2;
+constexpr int kNumEpi = 12;       // three per TMEM lane quarter
+constexpr int kThreads = 32 * (kEpi0 + kNumEpi);
+
+constexpr int kRows = 64;                      // tokens per CTA
+constexpr int kTileTokens = 2 * kRows;
+constexpr int kK = 64;                         // input fields per stage: one 128-byte row
+constexpr int kBox = kRows * 128;              // one coordinate of A
+constexpr int kABytes = 2 * kBox;
+constexpr int kMaxSlots = 8;
+constexpr int kCtrl = 256;
+constexpr int kSmemLimit = 232448;
+constexpr int kCoStep = 32;                    // N = co is a multiple of 32 with cta_group::2
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kSleep = 64;
+
+// Most output fields per group: all coordinates of a unit in TMEM.
+__host__ __device__ inline int co_most(int N) {
+  const int co = 2 * (int)kTmemCols / N / kCoStep * kCoStep;
+  return co < 128 ? co : 128;
+}
+// Output fields in 32-field blocks (the last may be padding in part: zero
+// weights, no stores), dealt out evenly to the groups.
+struct Groups {
+  int blocks, n;
+  __host__ __device__ Groups(int F_out, int N) {
+    blocks = (F_out + kCoStep - 1) / kCoStep;
+    n = (blocks * kCoStep + co_most(N) - 1) / co_most(N);
+  }
+  __host__ __device__ int co(int g) const { return kCoStep * (blocks / n + (g < blocks % n ? 1 : 0)); }
+  __host__ __device__ int first(int g) const {
+    const int r = blocks % n;
+    return kCoStep * (g * (blocks / n) + (g < r ? g : r));
+  }
+};
+// Stages of 64 input fields: the real bins 0 and N / 2, then the complex bins.
+__host__ __device__ inline int num_complex(int N) { return (N - 1) / 2; }
+__host__ __device__ inline bool has_mid(int N) { return N > 1 && N % 2 == 0; }
+__host__ __device__ inline int num_stages(int N) { return 1 + num_complex(N); }
+__host__ __device__ inline int k_blocks(int F_in) { return (F_in + kK - 1) / kK; }
+// First 128-byte row of the packed weights of (group, 64 input fields kb, stage,
+// CTA half); a half is co rows: W_0 of its co / 2 fields, then W_{N/2} (stage 0),
+// or Wi, then Wr.
+__host__ __device__ inline int64_t weight_row(const Groups &gr, int F_in, int N, int g, int kb, int st, int half) {
+  const int64_t per = (int64_t)k_blocks(F_in) * num_stages(N) * 2;
+  return per * gr.first(g) + (int64_t)((kb * num_stages(N) + st) * 2 + half) * gr.co(g);
+}
+// Width of S's rows: a multiple of 8 values (16 bytes), at least one box.
+__host__ __device__ inline int padded(int F) { return F < kK ? kK : (F + 7) / 8 * 8; }
+
+// ---------------------------------------------------------------- pre-pass
+
+// x [T][F][N] -> S[c][t][padded F], one thread per (token, two fields).
+template <int N, typename T, bool H>
+__global__ void __launch_bounds__(256)
+spectra_kernel(const T *__restrict__ x, uint32_t *__restrict__ S, int64_t Tn, int F, Trig trig) {
+  const int half = padded(F) / 2;
+  const int64_t n = Tn * half;
+  for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < n; p += (int64_t)gridDim.x * 256) {
+    const int64_t t = p / half;
+    const int f = 2 * (int)(p - t * half);
+    float a[N], b[N];
+#pragma unroll
+    for (int h = 0; h < N; ++h) a[h] = b[h] = 0.0f;
+    const T *src = x + ((size_t)t * F + f) * N;
+    if (f < F) load_field<N, T>(src, a);
+    if (f + 1 < F) load_field<N, T>(src + N, b);
+    float2 v[N], z[N];
+#pragma unroll
+    for (int h = 0; h < N; ++h) v[h] = make_float2(a[h], b[h]);
+    fwd_dft2<N>(v, z, trig);
+#pragma unroll
+    for (int c = 0; c < N; ++c) S[(size_t)c * n + p] = pack_x2<H>(z[c].x, z[c].y);
+  }
+}
+
+// ---------------------------------------------------------------- weights
+
+// W [F_out][F_in][N] (or, adjoint, V[o][i][m] = W[i][o][-m] of W [F_in][F_out][N],
+// whose spectrum is W[i][o]'s conjugate) -> the packed rows and the fp32 section
+// Ws[i][c][o] of the CUDA-core kernels, 1/N folded in (and, in the packed rows,
+// the 2 of the one-sided inverse).  A CTA takes 64 input fields x 8 outputs: a
+// warp one output, a lane two input fields; the fp32 values go through shared
+// memory so that both outputs are written in whole sectors.
+template <int N, typename T, bool H, bool ADJ>
+__global__ void __launch_bounds__(256)
+pack_gemm_kernel(const T *__restrict__ W, int F_in, int F_out, float *__restrict__ Ws, uint32_t *__restrict__ dst,
+                 Trig trig) {
+  __shared__ float sm[kK * N][9];
+  const Groups gr(F_out, N);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int kb = blockIdx.x, o0 = blockIdx.y * 8, o = o0 + warp, i = kb * kK + 2 * lane;
+  float a[N], b[N];
+#pragma unroll
+  for (int h = 0; h < N; ++h) a[h] = b[h] = 0.0f;
+  if (o < F_out) {
+    if (i < F_in) load_field<N, T>(W + (ADJ ? (size_t)i * F_out + o : (size_t)o * F_in + i) * N, a);
+    if (i + 1 < F_in) load_field<N, T>(W + (ADJ ? (size_t)(i + 1) * F_out + o : (size_t)o * F_in + i + 1) * N, b);
+  }
+  float2 v[N], z[N];
+#pragma unroll
+  for (int h = 0; h < N; ++h) v[h] = make_float2(a[h], b[h]);
+  fwd_dft2<N>(v, z, trig);
+  int g = 0;
+  while (g + 1 < gr.n && o >= gr.first(g + 1)) ++g;
+  const int hc = gr.co(g) / 2, hh = (o - gr.first(g)) / hc, r = (o - gr.first(g)) % hc;
+  const float inv_n = 1.0f / (float)N;
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const bool real = c == 0 || (has_mid(N) && c == N - 1);
+    const bool im = !real && c % 2 == 0;
+    const float2 w = scl2(z[c], ADJ && im ? -inv_n : inv_n);
+    sm[2 * lane * N + c][warp] = w.x;
+    sm[(2 * lane + 1) * N + c][warp] = w.y;
+    const float2 q = real ? w : scl2(w, 2.0f);
+    const int st = real ? 0 : (c + 1) / 2;
+    const int row = real ? (c == 0 ? r : hc + r) : (im ? r : hc + r);
+    dst[(weight_row(gr, F_in, N, g, kb, st, hh) + row) * 32 + lane] = pack_x2<H>(q.x, q.y);
+  }
+  if (!has_mid(N))   // stage 0's second half of rows is not used, but loaded
+    dst[(weight_row(gr, F_in, N, g, kb, 0, hh) + hc + r) * 32 + lane] = 0u;
+  __syncthreads();
+  for (int p = threadIdx.x; p < kK * N * 8; p += 256) {
+    const int ol = p & 7, ic = p >> 3, ii = kb * kK + ic / N;
+    if (ii < F_in && o0 + ol < F_out) Ws[((size_t)ii * N + ic % N) * F_out + o0 + ol] = sm[ic][ol];
+  }
+}
+
+// ---------------------------------------------------------------- product kernel
+
+struct GemmArgs {
+  void *out;
+  const void *dh;
+  unsigned int *fault;
+  unsigned int epoch;
+  int64_t T;
+  int N, F_in, F_out, units, nslots, slot_bytes, bufs, act;
+  Trig trig;
+};
+
+// One item of the epilogue: 16 token rows x 8 columns of every coordinate; a
+// thread has fields f, f + 1 (kEpiGated, kEpiGates: a gate and its value) of
+// tokens tok0, tok0 + 8.
+template <int N, bool H, int EPI>
+__device__ __forceinline__ void gemm_epilogue(uint32_t tb, int half, int64_t tok0, int f, const GemmArgs &args) {
+  using namespace tc;
+  using T = typename std::conditional<H, __half, __nv_bfloat16>::type;
+  const int F_out = args.F_out;
+  const bool real_field = f < F_out;
+  uint32_t v[N][4];
+#pragma unroll
+  for (int k = 0; k < N; ++k) tmem_ld_16x256b(tb + (uint32_t)(k * half), v[k]);
+  tmem_wait_ld();
+  T *out = static_cast<T *>(args.out);
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int64_t tok = tok0 + 8 * r;
+    if (tok >= args.T || !real_field) continue;
+    float2 z[N], p[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      // column groups: Y_0, (Y_{N/2},) then Im, Re of each complex bin
+      constexpr int first = N > 1 && N % 2 == 0 ? 2 : 1;
+      const int b = (k - first) / 2 + 1;
+      const int c = k == 0 ? 0 : (k < first ? N - 1 : ((k - first) % 2 == 0 ? 2 * b : 2 * b - 1));
+      z[c] = make_float2(__uint_as_float(v[k][2 * r]), __uint_as_float(v[k][2 * r + 1]));
+    }
+    inv_dft2<N>(z, p, args.trig);
+    if constexpr (EPI == kEpiLinear) {
+      float y[N];
+#pragma unroll
+      for (int s = 0; s < N; ++s) y[s] = p[s].x;
+      store_field<N, T>(out + ((size_t)tok * F_out + f) * N, y);
+      if (f + 1 < F_out) {
+#pragma unroll
+        for (int s = 0; s < N; ++s) y[s] = p[s].y;
+        store_field<N, T>(out + ((size_t)tok * F_out + f + 1) * N, y);
+      }
+    } else {
+      const size_t at = ((size_t)tok * (F_out >> 1) + (f >> 1)) * N;
+      float d[N];
+      if constexpr (EPI == kEpiGates) load_field<N, T>(static_cast<const T *>(args.dh) + at, d);
+#pragma unroll
+      for (int s = 0; s < N; s += 2) {   // two slots at a time
+        const int e = s + 1 < N ? s + 1 : s;
+        const float2 g = make_float2(p[s].x, p[e].x), u = make_float2(p[s].y, p[e].y);
+        float2 a = g, slope = make_float2(1.0f, 1.0f);
+        if constexpr (EPI == kEpiGated) {
+          if (args.act == EQLIN_ACT_SILU) a = silu2(g);
+          if (args.act == EQLIN_ACT_GELU) a = gelu_erf2(g);
+          d[s] = a.x * u.x;
+          d[e] = a.y * u.y;
+        } else {
+          if (args.act == EQLIN_ACT_SILU) slope = silu_slope2(g, a);
+          if (args.act == EQLIN_ACT_GELU) slope = gelu_slope2(g, a);
+          const float2 dd = make_float2(d[s], d[e]);
+          const float2 dg = mul2(mul2(dd, u), slope), du = mul2(dd, a);
+          p[s] = make_float2(dg.x, du.x);
+          p[e] = make_float2(dg.y, du.y);
+        }
+      }
+      if constexpr (EPI == kEpiGated) {
+        store_field<N, T>(out + at, d);
+      } else {
+        float y[N];
+#pragma unroll
+        for (int s = 0; s < N; ++s) y[s] = p[s].x;
+        store_field<N, T>(out + 2 * at, y);
+#pragma unroll
+        for (int s = 0; s < N; ++s) y[s] = p[s].y;
+        store_field<N, T>(out + 2 * at + N, y);
+      }
+    }
+  }
+  __syncwarp();
+}
+
+template <bool H, int EPI>
+__device__ __forceinline__ void gemm_epilogue_n(uint32_t tb, int half, int64_t tok0, int f, const GemmArgs &args) {
+  switch (args.N) {   // uniform
+#define EQLIN_CASE(NN)                                       \
+  case NN:                                                   \
+    gemm_epilogue<NN, H, EPI>(tb, half, tok0, f, args);      \
+    break;
+    EQLIN_CASE(1) EQLIN_CASE(2) EQLIN_CASE(3) EQLIN_CASE(4) EQLIN_CASE(5) EQLIN_CASE(6)
+    EQLIN_CASE(7) EQLIN_CASE(8) EQLIN_CASE(9) EQLIN_CASE(10) EQLIN_CASE(11) EQLIN_CASE(12)
+    EQLIN_CASE(13) EQLIN_CASE(14) EQLIN_CASE(15) EQLIN_CASE(16)
+#undef EQLIN_CASE
+  }
+}
+
+template <bool H, int EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+    spectral_gemm_kernel(const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_big,
+                         const __grid_constant__ CUtensorMap map_small, const __grid_constant__ GemmArgs args) {
+  using namespace tc;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *const gbase = smem_raw + (base - raw);
+  const int nslots = args.nslots;
+  const uint32_t slot_bytes = (uint32_t)args.slot_bytes;
+  const uint32_t sBar = base + (uint32_t)nslots * slot_bytes;
+  auto bar_full = [&](int s) { return sBar + 8u * s; };                    // both CTAs' stage landed (leader)
+  auto bar_empty = [&](int s) { return sBar + 8u * (kMaxSlots + s); };     // the slot's MMAs are done
+  auto bar_acc_full = [&](int b) { return sBar + 8u * (2 * kMaxSlots + b); };
+  auto bar_acc_empty = [&](int b) { return sBar + 8u * (2 * kMaxSlots + 2 + b); };   // leader
+  const uint32_t tmem_slot = sBar + 8u * (2 * kMaxSlots + 4);
+  static_assert(8 * (2 * kMaxSlots + 4) + 4 <= kCtrl, "control block");
+  volatile uint32_t *tmem_slot_ptr = reinterpret_cast<volatile uint32_t *>(gbase + (tmem_slot - base));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const FaultCtx fault{args.fault, args.epoch};
+  const int N = args.N, F_in = args.F_in;
+  const Groups gr(args.F_out, N);
+  const int nkb = k_blocks(F_in), nst = num_stages(N);
+  const uint32_t bufs = (uint32_t)args.bufs;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_acc_full(b), 1);
+      mbar_init(bar_acc_empty(b), 2 * kNumEpi);
+    }
+    fence_mbarrier_init_cluster();
+  }
+  if (warp == kProd) tmem_alloc_pair(tmem_slot, kTmemCols);
+  tcgen05_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tcgen05_fence_after();
+  const uint32_t tmem_base = *tmem_slot_ptr;
+
+  // unit n of this pair: neighbouring pairs take a tile's groups side by side, so
+  // that the tile's spectra come from L2 after their first reading.  Where every
+  // round of the pairs takes whole tiles, a pair's group changes from round to
+  // round (the groups' sizes may differ).
+  const int nunits = args.units > pair ? (args.units - pair + npairs - 1) / npairs : 0;
+  auto unit_tile = [&](int n) { return (pair + n * npairs) / gr.n; };
+  auto unit_group = [&](int n) { return (pair + n * npairs + (npairs % gr.n == 0 ? n : 0)) % gr.n; };
+  // the accumulator buffer of unit n and its phase
+  auto acc_buf = [&](int n) { return bufs == 2 ? (uint32_t)n & 1u : 0u; };
+  auto acc_phase = [&](int n) { return (bufs == 2 ? (uint32_t)n >> 1 : (uint32_t)n) & 1u; };
+
+  if (warp == kProd) {
+    if (elect_one_sync()) {
+      prefetch_tensormap(&map_s);
+      prefetch_tensormap(&map_big);
+      prefetch_tensormap(&map_small);
+      const uint32_t leader_full = mapa_shared(bar_full(0), 0);
+      const int co_big = gr.co(0);
+      uint32_t s = 0, ph = 0;
+      bool ok = true;
+      for (int n = 0; n < nunits && ok; ++n) {
+        const int g = unit_group(n), co = gr.co(g);
+        const int row0 = unit_tile(n) * kTileTokens + (int)rank * kRows;
+        int brow = (int)weight_row(gr, F_in, N, g, 0, 0, (int)rank);
+        const void *mb = co == co_big ? &map_big : &map_small;
+        for (int kb = 0; kb < nkb && ok; ++kb)
+          for (int st = 0; st < nst; ++st, brow += 2 * co) {
+            if (!mbar_wait_bounded(bar_empty(s), ph ^ 1u, fault, FAULT_WAIT_B_EMPTY, kWaitNs)) {
+              ok = false;
+              break;
+            }
+            const uint32_t slot = base + s * slot_bytes, full = leader_full + 8u * s;
+            const bool two = st > 0 || has_mid(N);
+            if (leader) mbar_arrive_expect_tx(bar_full(s), 2u * (uint32_t)((two ? kABytes : kBox) + 128 * co));
+            // rows of S: coordinate c of token t is row c T + t; rows past a
+            // tile's last token belong to outputs that are not stored
+            const int c0 = st == 0 ? 0 : 2 * st - 1, c1 = st == 0 ? N - 1 : 2 * st;
+            tma_load_2d_pair(slot, &map_s, full, kb * kK, (int)(c0 * args.T) + row0);
+            if (two) tma_load_2d_pair(slot + kBox, &map_s, full, kb * kK, (int)(c1 * args.T) + row0);
+            tma_load_2d_pair(slot + kABytes, mb, full, 0, brow);
+            if (++s == (uint32_t)nslots) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMma) {
+    if (leader) {
+      const uint64_t a0 = smem_desc_kmajor_sw128(base);
+      const uint32_t d_hi = (uint32_t)(a0 >> 32);      // the same for B
+      uint32_t s = 0, ph = 0;
+      bool ok = true;
+      for (int n = 0; n < nunits && ok; ++n) {
+        const int co = gr.co(unit_group(n));
+        const uint32_t half = (uint32_t)co / 2, b = acc_buf(n);
+        const uint32_t id_n = H ? idesc_f16_f32(128, co) : idesc_bf16_f32(128, co);
+        const uint32_t id_w = H ? idesc_f16_f32(128, 2 * co) : idesc_bf16_f32(128, 2 * co);
+        const uint32_t d0 = tmem_base + b * (kTmemCols / 2);
+        if (!mbar_wait_bounded_warp(bar_acc_empty(b), acc_phase(n) ^ 1u, fault, FAULT_WAIT_ACC_EMPTY, kWaitNs)) {
+          ok = false;
+          break;
+        }
+        tcgen05_fence_after();
+        for (int kb = 0; kb < nkb && ok; ++kb) {
+          const int left = (F_in - kb * kK + 15) / 16, ks = left < 4 ? left : 4;   // K-steps of 16 fields
+          for (int st = 0; st < nst; ++st) {
+            if (!mbar_wait_bounded_warp(bar_full(s), ph, fault, FAULT_WAIT_A_FULL, kWaitNs)) {
+              ok = false;
+              break;
+            }
+            tcgen05_fence_after();
+            if (elect_one_sync()) {
+              const uint32_t lo = (uint32_t)a0 + s * (slot_bytes >> 4);
+              for (int k = 0; k < ks; ++k) {
+                const uint32_t acc = kb > 0 || k > 0 ? 1u : 0u;
+                const uint32_t a_re = lo + 2u * k, a_im = a_re + (kBox >> 4), w = a_re + (kABytes >> 4);
+                const uint32_t w2 = w + half * 8u;     // the second half of the rows (128 bytes each)
+                if (st == 0) {
+                  mma_bf16_pair_w(d0, a_re, d_hi, w, d_hi, id_n, acc);
+                  if (has_mid(N)) mma_bf16_pair_w(d0 + half, a_im, d_hi, w2, d_hi, id_n, acc);
+                } else {
+                  const uint32_t d = d0 + (uint32_t)((has_mid(N) ? 2 : 1) + 2 * (st - 1)) * half;
+                  mma_bf16_pair_w(d, a_re, d_hi, w, d_hi, id_w, acc);                          // [Im|Re] += Re X [Wi;Wr]
+                  mma_bf16_pair_w(d, a_im, d_hi, w2, d_hi, id_n, 1u);                          // Im += Im X Wr
+                  mma_bf16_pair_w(d + half, a_im, d_hi, w, d_hi, id_n | (1u << 14), 1u);       // Re -= Im X Wi
+                }
+              }
+              mma_commit_pair_mc(bar_empty(s), 0x3);
+            }
+            __syncwarp();
+            if (++s == (uint32_t)nslots) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        if (!ok) break;
+        if (elect_one_sync()) mma_commit_pair_mc(bar_acc_full(b), 0x3);
+        __syncwarp();
+      }
+    }
+  } else {
+    // TMEM lane quarter q4 holds token rows 32 (q4 % 2) .. of this CTA and the
+    // group's fields of half q4 / 2; its items (16 rows x 8 columns) go round its
+    // three warps
+    const int q4 = warp & 3, h = q4 >> 1;
+    const uint32_t leader_acc_empty = mapa_shared(bar_acc_empty(0), 0);
+    bool ok = true;
+    for (int n = 0; n < nunits && ok; ++n) {
+      const int g = unit_group(n), half = gr.co(g) / 2;
+      const uint32_t b = acc_buf(n);
+      const int64_t tok0 = (int64_t)unit_tile(n) * kTileTokens + (int64_t)rank * kRows + (q4 & 1) * 32;
+      const int f0 = gr.first(g) + h * half;
+      if constexpr (EPI == kEpiGates) {
+        // dh of this quarter's rows and fields, into L2 while the products run
+        const int hidden = args.F_out >> 1;
+        const int j0 = f0 >> 1, j1 = (f0 + half) >> 1 < hidden ? (f0 + half) >> 1 : hidden;
+        const int64_t t = tok0 + lane;
+        if ((warp - kEpi0) < 4 && t < args.T && j0 < j1) {
+          const char *src = static_cast<const char *>(args.dh) + ((size_t)t * hidden + j0) * N * 2;
+          const int bytes = (j1 - j0) * N * 2;
+          for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + o));
+        }
+      }
+      if (!mbar_wait_bounded(bar_acc_full(b), acc_phase(n), fault, FAULT_WAIT_ACC_FULL, kWaitNs, kSleep)) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      tcgen05_fence_after();
+      for (int i = (warp - kEpi0) >> 2; i < half / 4; i += kNumEpi / 4) {
+        const int sub = i & 1, fg = (i >> 1) * 8;
+        gemm_epilogue_n<H, EPI>(tmem_base + ((uint32_t)(q4 * 32 + sub * 16) << 16) + b * (kTmemCols / 2) + (uint32_t)fg,
+                                half, tok0 + sub * 16 + (lane >> 2), f0 + fg + 2 * (lane & 3), args);
+      }
+      tcgen05_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(leader_acc_empty + 8u * b);
+    }
+  }
+
+  __syncwarp();
+  if (fault_raised(fault)) {   // give copies still in flight time to land
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
+  tcgen05_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == kProd) {
+    tcgen05_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+struct DevCache {
+  int clusters[2][3] = {};
+};
+std::mutex g_mu;
+DevCache g_cache[64];
+
+template <bool H, int EPI>
+int launch_gemm(const void *S, const void *pack, const void *dh, void *out, int64_t T, int N, int F_in, int F_out,
+                int act, cudaStream_t s) {
+  auto kern = spectral_gemm_kernel<H, EPI>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+    return set_error(EQLIN_ERR_CUDA, "cudaGetDevice failed");
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int maxc = 0;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    int &n = g_cache[dev].clusters[H][EPI];
+    if (!n) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+      if (e != cudaSuccess) return set_error(EQLIN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      cfg.gridDim = dim3(2, 1, 1);
+      cfg.dynamicSmemBytes = kSmemLimit;
+      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess || n <= 0) {
+        n = 0;
+        return set_error(EQLIN_ERR_CUDA, "cudaOccupancyMaxActiveClusters: %s", cudaGetErrorString(e));
+      }
+    }
+    maxc = n;
+  }
+  const Groups gr(F_out, N);
+  const int co_big = gr.co(0), co_small = gr.co(gr.n - 1);
+  CUtensorMap ms, mb, mt;
+  int rc = tma_map_2d_bf16(&ms, S, (uint64_t)padded(F_in), (uint64_t)T * N, (uint64_t)padded(F_in) * 2, kK, kRows, true);
+  if (rc) return rc;
+  const uint64_t rows = (uint64_t)weight_row(gr, F_in, N, gr.n - 1, k_blocks(F_in), 0, 0);
+  rc = tma_map_2d_bf16(&mb, pack, kK, rows, 128, kK, (uint32_t)co_big, true);
+  if (rc) return rc;
+  rc = tma_map_2d_bf16(&mt, pack, kK, rows, 128, kK, (uint32_t)co_small, true);
+  if (rc) return rc;
+  GemmArgs a;
+  rc = fault_word_address(&a.fault);
+  if (rc) return rc;
+  a.out = out;
+  a.dh = dh;
+  a.epoch = next_launch_epoch();
+  a.T = T;
+  a.N = N;
+  a.F_in = F_in;
+  a.F_out = F_out;
+  a.act = act;
+  a.trig = make_trig(N);
+  a.units = (int)((T + kTileTokens - 1) / kTileTokens) * gr.n;
+  a.bufs = N * co_big <= (int)kTmemCols ? 2 : 1;
+  a.slot_bytes = kABytes + 128 * co_big;
+  a.nslots = (kSmemLimit - 1024 - kCtrl) / a.slot_bytes;
+  if (a.nslots > kMaxSlots) a.nslots = kMaxSlots;
+  int npairs = maxc / gr.n * gr.n;   // whole tiles per round, where there are that many pairs
+  if (npairs < 1) npairs = maxc;
+  if (npairs > a.units) npairs = a.units;
+  cfg.gridDim = dim3(2 * npairs, 1, 1);
+  cfg.dynamicSmemBytes = 1024 + (size_t)a.nslots * a.slot_bytes + kCtrl;
+  cfg.stream = s;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ms, mb, mt, a);
+  if (e != cudaSuccess) return set_error(EQLIN_ERR_CUDA, "spectral GEMM launch: %s", cudaGetErrorString(e));
+  return check_launch("spectral_gemm_kernel");
+}
+
+template <int N, typename T, bool H>
+int launch_spectra(const void *x, void *S, int64_t Tn, int F, cudaStream_t s) {
+  const int64_t n = Tn * (padded(F) / 2), want = (n + 255) / 256;
+  const unsigned grid = (unsigned)(want < 148 * 16 ? want : 148 * 16);
+  spectra_kernel<N, T, H><<<grid, 256, 0, s>>>(static_cast<const T *>(x), static_cast<uint32_t *>(S), Tn, F, make_trig(N));
+  return check_launch("half spectra");
+}
+
+template <int N, typename T, bool H>
+int launch_pack(const void *W, int F_in, int F_out, bool adjoint, void *Ws, void *dst, cudaStream_t s) {
+  const dim3 grid((unsigned)k_blocks(F_in), (unsigned)(Groups(F_out, N).blocks * kCoStep / 8));
+  if (grid.y > 65535) return set_error(EQLIN_ERR_UNSUPPORTED, "channel count too large");
+  const T *w = static_cast<const T *>(W);
+  if (adjoint)
+    pack_gemm_kernel<N, T, H, true><<<grid, 256, 0, s>>>(w, F_in, F_out, static_cast<float *>(Ws),
+                                                         static_cast<uint32_t *>(dst), make_trig(N));
+  else
+    pack_gemm_kernel<N, T, H, false><<<grid, 256, 0, s>>>(w, F_in, F_out, static_cast<float *>(Ws),
+                                                          static_cast<uint32_t *>(dst), make_trig(N));
+  return check_launch("spectral GEMM weight packing");
+}
+
+}  // namespace
+
+bool gemm_tc_supported(int N, int F_in, int F_out, int dtype) {
+  return (dtype == EQLIN_BF16 || dtype == EQLIN_F16) && N >= 1 && N <= kMaxN && F_in >= 16 && F_out >= 1 &&
+         F_in <= (1 << 15) && F_out <= (1 << 15);
+}
+
+size_t gemm_tc_bytes(int N, int F_in, int F_out) {
+  const Groups gr(F_out, N);
+  return (size_t)weight_row(gr, F_in, N, gr.n - 1, k_blocks(F_in), 0, 0) * 128;
+}
+
+size_t gemm_tc_spectra_bytes(int64_t T, int N, int F) { return (size_t)T * N * padded(F) * 2; }
+
+bool gemm_tc_tokens_ok(int64_t T, int N, int F_out) {
+  return T <= (int64_t)0x7fff0000LL / N && T <= (int64_t)0x7fff0000LL / Groups(F_out, N).n;
+}
+
+#define EQLIN_CASES                                                                              \
+  EQLIN_CASE(1) EQLIN_CASE(2) EQLIN_CASE(3) EQLIN_CASE(4) EQLIN_CASE(5) EQLIN_CASE(6)            \
+  EQLIN_CASE(7) EQLIN_CASE(8) EQLIN_CASE(9) EQLIN_CASE(10) EQLIN_CASE(11) EQLIN_CASE(12)         \
+  EQLIN_CASE(13) EQLIN_CASE(14) EQLIN_CASE(15) EQLIN_CASE(16)
+
+int launch_gemm_tc_spectra(const void *x, void *S, int64_t T, int N, int F, int dtype, cudaStream_t s) {
+  switch (N) {
+#define EQLIN_CASE(NN)                                                                           \
+  case NN:                                                                                       \
+    return dtype == EQLIN_F16 ? launch_spectra<NN, __half, true>(x, S, T, F, s)                  \
+                              : launch_spectra<NN, __nv_bfloat16, false>(x, S, T, F, s);
+    EQLIN_CASES
+#undef EQLIN_CASE
+  }
+  return set_error(EQLIN_ERR_UNSUPPORTED, "N=%d not in 1..16", N);
+}
+
+int launch_gemm_tc_pack(const void *W, int N, int F_in, int F_out, bool adjoint, int dtype, void *Ws, void *dst,
+                        cudaStream_t s) {
+  switch (N) {
+#define EQLIN_CASE(NN)                                                                           \
+  case NN:                                                                                       \
+    return dtype == EQLIN_F16 ? launch_pack<NN, __half, true>(W, F_in, F_out, adjoint, Ws, dst, s) \
+                              : launch_pack<NN, __nv_bfloat16, false>(W, F_in, F_out, adjoint, Ws, dst, s);
+    EQLIN_CASES
+#undef EQLIN_CASE
+  }
+  return set_error(EQLIN_ERR_UNSUPPORTED, "N=%d not in 1..16", N);
+}
+
+int launch_gemm_tc(int epi, const void *S, const void *pack, const void *dh, void *out, int64_t T, int N, int F_in,
+                   int F_out, int act, int dtype, cudaStream_t s) {
+  const bool f16 = dtype == EQLIN_F16;
+  if (epi == kEpiLinear)
+    return f16 ? launch_gemm<true, kEpiLinear>(S, pack, dh, out, T, N, F_in, F_out, act, s)
+               : launch_gemm<false, kEpiLinear>(S, pack, dh, out, T, N, F_in, F_out, act, s);
+  if (epi == kEpiGated)
+    return f16 ? launch_gemm<true, kEpiGated>(S, pack, dh, out, T, N, F_in, F_out, act, s)
+               : launch_gemm<false, kEpiGated>(S, pack, dh, out, T, N, F_in, F_out, act, s);
+  return f16 ? launch_gemm<true, kEpiGates>(S, pack, dh, out, T, N, F_in, F_out, act, s)
+             : launch_gemm<false, kEpiGates>(S, pack, dh, out, T, N, F_in, F_out, act, s);
+}
+
+}  // namespace eqlin

@@ -54,4 +54,19 @@ int launch_wide_tc_pack(const void *W, int F_in, int F_out, bool adjoint, int dt
 int launch_wide_tc(const void *x, const void *pack, void *y, int64_t T, int F_in, int F_out, int dtype,
                    cudaStream_t s);
 
+// Any N on tensor cores (gated_gemm_tc.cu), bf16 and fp16, at least 16 input
+// fields: the half spectra S of x [T][F][N] (gemm_tc_spectra_bytes, 256-byte
+// aligned), then the products with the packed weights (gemm_tc_bytes) of the layer
+// F_in -> F_out and epilogue `epi`.  The pack is W [F_out][F_in][N]'s or, with
+// adjoint, that of V[o][i][m] = W[i][o][-m]; Ws: the fp32 spectrum beside it.
+bool gemm_tc_supported(int N, int F_in, int F_out, int dtype);
+bool gemm_tc_tokens_ok(int64_t T, int N, int F_out);
+size_t gemm_tc_bytes(int N, int F_in, int F_out);
+size_t gemm_tc_spectra_bytes(int64_t T, int N, int F);
+int launch_gemm_tc_spectra(const void *x, void *S, int64_t T, int N, int F, int dtype, cudaStream_t s);
+int launch_gemm_tc_pack(const void *W, int N, int F_in, int F_out, bool adjoint, int dtype, void *Ws, void *dst,
+                        cudaStream_t s);
+int launch_gemm_tc(int epi, const void *S, const void *pack, const void *dh, void *out, int64_t T, int N, int F_in,
+                   int F_out, int act, int dtype, cudaStream_t s);
+
 }  // namespace eqlin

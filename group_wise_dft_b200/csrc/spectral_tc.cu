@@ -135,36 +135,40 @@ constexpr int kDftGroups = kNumDftWarps / kDftWarpsPerGroup;    // 5
 // is its busiest role, nor in the negacyclic mode, whose epilogue also reads
 // the even half's outputs and writes twice the bytes.
 constexpr int kEpiHelpGroups = kNumEpiWarps / kDftWarpsPerGroup;  // 4
-template <int MODE>
-__host__ __device__ constexpr bool epilogue_helps() { return MODE == kModeCyclic8 || MODE == kModeCyclic4; }
+template <int MODE, bool GATED = false>
+__host__ __device__ constexpr bool epilogue_helps() {
+  return !GATED && (MODE == kModeCyclic8 || MODE == kModeCyclic4);
+}
 // In the D8 and negacyclic modes it is the other way round: the epilogue
 // (back-transform and GELU of every output; or, for the odd half of C_16, the
 // even half's outputs read and twice the bytes written) paces the layer, and
 // transform warps 0..7 (two per TMEM lane quarter, as the epilogue warps) take
 // every other 8-column group of each chunk's epilogue; they transform the next
-// tile's block pairs before their share of a tile's last chunk.
+// tile's block pairs before their share of a tile's last chunk.  So too with the
+// gated layer's epilogues (GATED: an activation and a product per pair of
+// outputs, or their gradients), where a tile's transform serves many chunks.
 constexpr int kD8HelpWarps = 8;
-template <int MODE>
+template <int MODE, bool GATED = false>
 __host__ __device__ constexpr bool transform_warps_help_epilogue() {
-  return MODE == kModeD8 || MODE == kModeNegacyclic8;
+  return GATED || MODE == kModeD8 || MODE == kModeNegacyclic8;
 }
-template <int MODE>
+template <int MODE, bool GATED = false>
 __host__ __device__ constexpr int epilogue_warps() {
-  return kNumEpiWarps + (transform_warps_help_epilogue<MODE>() ? kD8HelpWarps : 0);
+  return kNumEpiWarps + (transform_warps_help_epilogue<MODE, GATED>() ? kD8HelpWarps : 0);
 }
 // Which two-warp group transforms block pair jp: with epilogue help, the
 // transform groups take jp < kDftGroups and the pairs after the helped ones
 // (from group 0 on, which finishes its first pair earliest) and the epilogue
 // groups the rest; without, transform group jp mod kDftGroups.
-template <int MODE>
+template <int MODE, bool GATED = false>
 __host__ __device__ constexpr bool pair_by_epilogue(int jp) {
-  return epilogue_helps<MODE>() && jp >= kDftGroups && jp < kDftGroups + kEpiHelpGroups;
+  return epilogue_helps<MODE, GATED>() && jp >= kDftGroups && jp < kDftGroups + kEpiHelpGroups;
 }
-template <int MODE>
+template <int MODE, bool GATED = false>
 __host__ __device__ constexpr int pair_group(int jp) {
-  if (!epilogue_helps<MODE>()) return jp % kDftGroups;
+  if (!epilogue_helps<MODE, GATED>()) return jp % kDftGroups;
   return jp < kDftGroups ? jp
-                         : (pair_by_epilogue<MODE>(jp) ? jp - kDftGroups : (jp - kEpiHelpGroups) % kDftGroups);
+                         : (pair_by_epilogue<MODE, GATED>(jp) ? jp - kDftGroups : (jp - kEpiHelpGroups) % kDftGroups);
 }
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAccBufCols = 256;
@@ -692,6 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap map_b_full,
                         const __grid_constant__ CUtensorMap map_b_last, const TcArgs args) {
   using namespace tc;
+  constexpr bool kGated = EPI != kEpiLinear;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -745,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_acc_full(i), kNumIssuers);
-      mbar_init(bar_acc_empty(i), 2 * epilogue_warps<MODE>());   // every epilogue warp of both CTAs
+      mbar_init(bar_acc_empty(i), 2 * epilogue_warps<MODE, kGated>());   // every epilogue warp of both CTAs
     }
     fence_mbarrier_init_cluster();
   }
@@ -1002,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t leader_a_full0 = mapa_shared(bar_a_full(0), 0);
     auto transform_tile = [&](int ti) -> bool {
       for (int jp = grp; jp < nstage; ++jp) {
-        if (pair_by_epilogue<MODE>(jp) || pair_group<MODE>(jp) != grp) continue;
+        if (pair_by_epilogue<MODE, kGated>(jp) || pair_group<MODE, kGated>(jp) != grp) continue;
         if (!mbar_wait_bounded(bar_x_full(jp), (uint32_t)ti & 1u, fault, FAULT_WAIT_X_FULL,
                                kWaitLimitNs, kSleepNs))
           return false;
@@ -1014,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    if constexpr (transform_warps_help_epilogue<MODE>()) {
+    if constexpr (transform_warps_help_epilogue<MODE, kGated>()) {
       // transform warps 0..kD8HelpWarps-1 also take the odd 8-column groups of
       // every chunk's epilogue; the next tile's block pairs are transformed
       // before the share of a tile's last chunk (whose buffer the next tile's
@@ -1048,7 +1053,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                              (q4 & 1) * 32 + sub * 16 + tr;
         const int field_base = c * kCoMax + h * half + 2 * tq;
         for (int fg = 8; fg < half; fg += 16) {
-          if constexpr (MODE == kModeD8)
+          if constexpr (kGated)
+            gated_epilogue_group<H, EPI>(tb, fg, half, tok0, field_base, args.T, F_out, ybase, args.y_even,
+                                         args.gelu);
+          else if constexpr (MODE == kModeD8)
             d8_epilogue_group<H>(tb, fg, half, tok0, field_base, args.T, F_out, ybase, args.gelu);
           else
             neg16_epilogue_group(tb, fg, half, tok0, field_base, args.T, F_out, ybase, args.y_even);
@@ -1061,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int ti = 0; ti < ntile_local && ok; ++ti) {
         for (int jp = grp; jp < nstage; ++jp) {
-          if (pair_by_epilogue<MODE>(jp) || pair_group<MODE>(jp) != grp) continue;
+          if (pair_by_epilogue<MODE, kGated>(jp) || pair_group<MODE, kGated>(jp) != grp) continue;
           if (!mbar_wait_bounded(bar_x_full(jp), (uint32_t)ti & 1u, fault, FAULT_WAIT_X_FULL,
                                  kWaitLimitNs, kSleepNs)) {
             ok = false;
@@ -1097,7 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ht = ((warp - kEpiWarp0) % kDftWarpsPerGroup) * 32 + lane;
     const uint32_t leader_a_full0 = mapa_shared(bar_a_full(0), 0);
     auto help_transform = [&](int ti) -> bool {
-      for (int jp = kDftGroups + hgrp; jp < nstage && pair_by_epilogue<MODE>(jp); jp += kEpiHelpGroups)
+      for (int jp = kDftGroups + hgrp; jp < nstage && pair_by_epilogue<MODE, kGated>(jp); jp += kEpiHelpGroups)
         if (!transform_pair_call<MODE, H>(gbase + (size_t)(2 * jp) * kBlockBytes, bar_x_full(jp),
                                           (uint32_t)ti & 1u, fault, ht, args.gelu,
                                           leader_a_full0 + 8u * (uint32_t)jp))
@@ -1109,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the first tile's helped block pairs before anything else; then, before
       // a tile's last chunk, whose epilogue the next tile's first chunk does
       // not wait for, the next tile's (with one chunk per tile, both at g = 0)
-      if constexpr (epilogue_helps<MODE>()) {
+      if constexpr (epilogue_helps<MODE, kGated>()) {
         const bool last_c = g % nchunks == nchunks - 1;
         const int h0 = g == 0 ? 0 : (last_c ? g / nchunks + 1 : ntile_local);
         const int h1 = last_c ? g / nchunks + 1 : 0;
@@ -1135,6 +1143,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                              (uint32_t)half1 * 16u);
         }
       }
+      if constexpr (EPI == kEpiGates) {
+        // likewise dh: half1 / 2 fields per token row
+        for (int g1 = g == 0 ? 0 : g + 1; g1 <= g + 1 && g1 < total_chunks; ++g1) {
+          const int c1 = g1 % nchunks;
+          const int half1 = chunk_fields(F_out, c1) >> 1;
+          const int64_t tok1 = (int64_t)(pair + (g1 / nchunks) * npairs) * kTileTokens +
+                               (int64_t)rank * kRowsPerCta + (q4 & 1) * 32 + sub * 16 + lane;
+          if (lane < 16 && tok1 < T)
+            bulk_prefetch_l2(static_cast<const uint8_t *>(args.y_even) +
+                                 ((size_t)tok1 * (F_out >> 1) + ((c1 * kCoMax + h * half1) >> 1)) * 16,
+                             (uint32_t)half1 * 8u);
+        }
+      }
       if (!mbar_wait_bounded(bar_acc_full(buf), ((uint32_t)g >> 1) & 1u, fault,
                              FAULT_WAIT_ACC_FULL, kWaitLimitNs, kSleepNs)) {
         ok = false;
@@ -1149,7 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int field_base = c * kCoMax + h * half + 2 * tq;
       // D8: the epilogue warps take the even 8-column groups, transform warps
       // 0..7 the odd ones (kD8HelpWarps)
-      for (int fg = 0; fg < half; fg += (transform_warps_help_epilogue<MODE>() ? 16 : 8)) {
+      for (int fg = 0; fg < half; fg += (transform_warps_help_epilogue<MODE, kGated>() ? 16 : 8)) {
         if constexpr (MODE == kModeD8) {
           d8_epilogue_group<H>(tb, fg, half, tok0, field_base, T, F_out, ybase, args.gelu);
           continue;

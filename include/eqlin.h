@@ -380,9 +380,14 @@ EQLIN_API int eqlin_d8_fourier_mlp(const void *z, const void *W1pack, const void
  * the *_workspace_bytes; their contents on entry do not matter.  Calls that
  * may overlap on the GPU need one each.
  *
- * Supported: 1 <= N <= 16, Cin, H >= 1, every dtype.  EQLIN_PATH_SIMT runs on
- * CUDA cores in fp32.  EQLIN_PATH_TC returns EQLIN_ERR_UNSUPPORTED where
- * eqlin_cyclic_gated_auto_path says EQLIN_PATH_SIMT. */
+ * Supported: 1 <= N <= 16, Cin, H >= 1, every dtype.  Paths: EQLIN_PATH_SIMT, on
+ * CUDA cores in fp32; EQLIN_PATH_TC, on tensor cores, for bf16 and fp16 with
+ * Cin >= 16 and H >= 8 (EQLIN_ERR_UNSUPPORTED otherwise): the half spectra of x,
+ * W and dp are rounded to `dtype` (fp16: sums of N values of x must not overflow
+ * it), fp32 accumulation.  AUTO takes the tensor cores for bf16 and more than a
+ * handful of tokens.  The forward needs a workspace on some of those shapes
+ * (eqlin_cyclic_gated_forward_workspace_bytes, 0 elsewhere); without it AUTO runs on
+ * CUDA cores and EQLIN_PATH_TC returns EQLIN_ERR_SIZE. */
 EQLIN_API size_t eqlin_cyclic_gated_spectrum_bytes(int N, int Cin, int H, int dtype);
 EQLIN_API int eqlin_cyclic_gated_weight_spectrum(const void *W, int N, int Cin, int H, int dtype, void *Wspec,
                                        size_t Wspec_bytes, eqlin_stream_t stream);
@@ -390,8 +395,10 @@ EQLIN_API size_t eqlin_cyclic_gated_adjoint_bytes(int N, int Cin, int H, int dty
 EQLIN_API int eqlin_cyclic_gated_weight_spectrum_adjoint(const void *W, int N, int Cin, int H, int dtype,
                                                void *Wspec_adj, size_t Wspec_adj_bytes, eqlin_stream_t stream);
 EQLIN_API int eqlin_cyclic_gated_auto_path(int N, int Cin, int H, int dtype);
+EQLIN_API size_t eqlin_cyclic_gated_forward_workspace_bytes(int64_t T, int N, int Cin, int H, int dtype);
 EQLIN_API int eqlin_cyclic_gated_forward(const void *x, const void *Wspec, void *h, int64_t T, int N, int Cin,
-                               int H, int act, int dtype, int path, eqlin_stream_t stream);
+                               int H, int act, int dtype, int path, void *workspace, size_t workspace_bytes,
+                               eqlin_stream_t stream);
 EQLIN_API size_t eqlin_cyclic_gated_backward_workspace_bytes(int64_t T, int N, int Cin, int H, int dtype);
 EQLIN_API int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec, const void *Wspec_adj,
                                 void *dx, void *dW, int64_t T, int N, int Cin, int H, int act, int dtype,

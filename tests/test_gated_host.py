@@ -21,8 +21,8 @@ def adj(W=P, N=6, C=10, H=5, dtype=0, out=P, bytes_=BIG):
     return L.eqlin_cyclic_gated_weight_spectrum_adjoint(W, N, C, H, dtype, out, bytes_, None)
 
 
-def fwd(x=P, spec=P, h=P, T=9, N=6, C=10, H=5, act=1, dtype=0, path=0):
-    return L.eqlin_cyclic_gated_forward(x, spec, h, T, N, C, H, act, dtype, path, None)
+def fwd(x=P, spec=P, h=P, T=9, N=6, C=10, H=5, act=1, dtype=0, path=0, ws=None, bytes_=0):
+    return L.eqlin_cyclic_gated_forward(x, spec, h, T, N, C, H, act, dtype, path, ws, bytes_, None)
 
 
 def bwd(x=P, dh=P, spec=P, adj=P, dx=P, dW=P, T=9, N=6, C=10, H=5, act=1, dtype=0, path=0, ws=P, bytes_=BIG):
@@ -48,6 +48,7 @@ def test_shapes(args, code):
     assert L.eqlin_cyclic_gated_spectrum_bytes(*shape) == 0
     assert L.eqlin_cyclic_gated_adjoint_bytes(*shape) == 0
     assert L.eqlin_cyclic_gated_auto_path(*shape) == -1
+    assert L.eqlin_cyclic_gated_forward_workspace_bytes(9, *shape) == 0
     assert L.eqlin_cyclic_gated_backward_workspace_bytes(9, *shape) == 0
 
 
@@ -87,6 +88,21 @@ def test_spectrum_buffers(call):
     assert call(W=MIS) == eq.EQLIN_ERR_ALIGN
     assert call(out=MIS) == eq.EQLIN_ERR_ALIGN
     assert call(bytes_=128) == eq.EQLIN_ERR_SIZE
+
+
+def test_forward_workspace():
+    """Some tensor-core shapes need one; they are refused without it when asked for."""
+    need = L.eqlin_cyclic_gated_forward_workspace_bytes(100, 16, 96, 64, eq.EQLIN_BF16)
+    assert need >= 100 * 96 * 16 * 2 and need % 256 == 0
+    assert L.eqlin_cyclic_gated_forward_workspace_bytes(100, 8, 96, 64, eq.EQLIN_BF16) == 0
+    assert L.eqlin_cyclic_gated_forward_workspace_bytes(100, 16, 96, 64, eq.EQLIN_F32) == 0
+    tc = dict(T=100, N=16, C=96, H=64, dtype=eq.EQLIN_BF16, path=eq.PATH_TC)
+    assert fwd(**tc) == eq.EQLIN_ERR_SIZE
+    assert fwd(**tc, ws=P, bytes_=need - 1) == eq.EQLIN_ERR_SIZE
+    assert fwd(**tc, ws=ctypes.c_void_p(0x1010), bytes_=need) == eq.EQLIN_ERR_SIZE
+    # T past what the kernels index: refused, not cut
+    assert fwd(T=1 << 31, N=16, C=96, H=64, dtype=eq.EQLIN_BF16, path=eq.PATH_TC, ws=P, bytes_=BIG) == \
+        eq.EQLIN_ERR_UNSUPPORTED
 
 
 def test_binding_refuses_bad_tensors():

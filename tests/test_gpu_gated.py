@@ -136,6 +136,23 @@ def test_tensor_cores_when_asked_for(T, C, H, act):
     run(T % 32 + 1, C, H, 8, BF16, act, path=eq.PATH_TC, halves=(2, 2.5, 2.5))
 
 
+# the two-pass products: every N, ragged fields and tokens, one or several groups of outputs and blocks of inputs
+GEMM = [(40, 16, 8, 5, "silu"), (129, 37, 101, 6, "gelu"), (257, 64, 40, 4, "silu"), (300, 96, 384, 16, "gelu"),
+        (1000, 100, 200, 12, "silu"), (700, 33, 19, 3, "none"), (130, 130, 70, 16, "silu"), (500, 200, 150, 8, "silu"),
+        (333, 24, 31, 8, "gelu"), (90, 65, 30, 2, "silu"), (64, 70, 90, 1, "silu"), (20 * 148 * 64 + 3, 20, 30, 7, "gelu")]
+
+
+@pytest.mark.parametrize("T,C,H,N,act", GEMM)
+def test_two_pass_products(T, C, H, N, act):
+    run(T, C, H, N, BF16, act, path=eq.PATH_TC, halves=(2, 2.5, 2.5))
+
+
+@pytest.mark.parametrize("N", range(1, 17))
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_two_pass_products_every_group(N, dtype):
+    run(150, 18, 9, N, dtype, "silu", path=eq.PATH_TC, seed=N, halves=(2, 2.5, 2.5))
+
+
 def test_outputs_at_odd_addresses():
     """h and dx 16 bytes off a 32-byte boundary: written whole, or refused when the tensor cores are asked for."""
     T, C, H = 200, 32, 48
