@@ -586,7 +586,7 @@ __device__ __forceinline__ void d8_epilogue_group(uint32_t tb, int fg, int half,
 // of a thread's item are one pair).  kEpiGated writes h = act(gate) value, 16
 // bytes per item; kEpiGates reads dh there and writes the pair's gradients
 // (dh value act'(gate), dh act(gate)), 32 contiguous bytes.  The activations
-// are the paired forms of tc_transforms.cuh: exact to far below the operand
+// are the paired forms of tc_transforms.cuh: good to well below the operand
 // rounding of the products.  Not inlined, as neg16_epilogue_group.
 template <bool H, int EPI>
 __device__ __noinline__ void gated_epilogue_group(uint32_t tb, int fg, int half, int64_t tok0, int field_base,
@@ -619,7 +619,7 @@ __device__ __noinline__ void gated_epilogue_group(uint32_t tb, int fg, int half,
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float2 g = make_float2(p[2 * q].x, p[2 * q + 1].x), u = make_float2(p[2 * q].y, p[2 * q + 1].y);
-        const float2 a = flags & kActSilu ? silu2(g) : (flags & kActGelu ? gelu_erf2(g) : g);
+        const float2 a = flags & kActSilu ? (H ? silu2(g) : silu_tanh2(g)) : (flags & kActGelu ? gelu_erf2(g) : g);
         const float2 h = mul2(a, u);
         w[q] = pack_x2<H>(h.x, h.y);
       }
@@ -634,7 +634,7 @@ __device__ __noinline__ void gated_epilogue_group(uint32_t tb, int fg, int half,
         const float2 d = unpack_x2<H>(dw[q]);
         float2 a = g, s = make_float2(1.0f, 1.0f);
         if (flags & kActSilu)
-          s = silu_slope2(g, a);
+          s = H ? silu_slope2(g, a) : silu_slope_tanh2(g, a);
         else if (flags & kActGelu)
           s = gelu_slope2(g, a);
         const float2 dg = mul2(mul2(d, u), s), du = mul2(d, a);
