@@ -14,17 +14,21 @@
 //
 // Everything is bound by memory.  Two forms:
 //  - an item of at most 32 kRowVecs vectors (a token, S = 1, or a tiny map) is
-//    one warp's: its values stay in registers, so they are read once, and the
-//    variance is the plain two-pass one;
+//    one warp's: its values stay in registers as they came (packed: more warps
+//    fit, and their loads are what hides the latency), so they are read once, and
+//    the variance is the plain two-pass one;
 //  - larger items are split into chunks of positions.  A CTA walks its chunk
-//    with one thread per vector of channels (memory order, whole lines), every
-//    value going into a running mean and sum of squared deviations (no
-//    cancellation, whatever the mean), which are joined per group by the
-//    pairwise update of Chan, Golub and LeVeque.  A second launch joins the
-//    chunks and normalises.
+//    with one thread per vector of channels (memory order, whole lines), a few
+//    positions at a time: their mean and squared deviations are exact two-pass
+//    sums in registers, joined by the pairwise update of Chan, Golub and LeVeque
+//    (no cancellation, whatever the mean).  A second pass joins the chunks and
+//    normalises.  The items go in batches that fit L2, and one launch takes the
+//    statistics of batch k and normalises batch k - 1, so that the second reading
+//    of x comes from L2 while the first of the next batch comes from memory.
 // Statistics, sums and all arithmetic are fp32; every sum has a fixed order.
 #include "activations.cuh"
 #include "eqlin_internal.cuh"
+#include "tc_transforms.cuh"
 
 namespace eqlin {
 namespace {
@@ -42,6 +46,7 @@ struct GnShape {
   int vec;          // values per vector
   int chunks;       // per item (chunk kernels)
   int64_t per;      // positions per chunk
+  int64_t batch;    // items per launch
 };
 
 template <int BYTES> struct VecOf;
@@ -50,26 +55,69 @@ template <> struct VecOf<8> { typedef uint2 type; };
 template <> struct VecOf<4> { typedef uint32_t type; };
 template <> struct VecOf<2> { typedef uint16_t type; };
 
+// V consecutive values as they lie in memory, and as pairs of fp32 (with V = 1
+// the second lane is a copy that the sums leave out).
 template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T *p, float (&v)[V]) {
+struct Raw {
   typedef typename VecOf<V * sizeof(T)>::type Q;
-  union { Q q; T e[V]; } u;
-  u.q = __ldg(reinterpret_cast<const Q *>(p));
-#pragma unroll
-  for (int k = 0; k < V; ++k) v[k] = to_f32(u.e[k]);
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T *p, const float (&v)[V]) {
-  typedef typename VecOf<V * sizeof(T)>::type Q;
-  union { Q q; T e[V]; } u;
-#pragma unroll
-  for (int k = 0; k < V; ++k) u.e[k] = from_f32<T>(v[k]);
-  *reinterpret_cast<Q *>(p) = u.q;
-}
+  union {
+    Q q;
+    T e[V];
+  };
+};
+template <int V> constexpr int pairs() { return (V + 1) / 2; }
 
-__device__ __forceinline__ float slope_any(int act, float z) {
-  float unused;
-  return eqlin::slope_any(act, z, unused);
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T *p) {
+  Raw<T, V> r;
+  r.q = __ldg(reinterpret_cast<const typename Raw<T, V>::Q *>(p));
+  return r;
+}
+// (a last reading: not kept in L2)
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_last(const T *p) {
+  Raw<T, V> r;
+  r.q = __ldcs(reinterpret_cast<const typename Raw<T, V>::Q *>(p));
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V> &r, float2 (&v)[pairs<V>()]) {
+#pragma unroll
+  for (int k = 0; k < pairs<V>(); ++k) v[k] = make_float2(to_f32(r.e[2 * k]), to_f32(r.e[V == 1 ? 0 : 2 * k + 1]));
+}
+// Written past L2's working set.
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T *p, const float2 (&v)[pairs<V>()]) {
+  Raw<T, V> r;
+#pragma unroll
+  for (int k = 0; k < pairs<V>(); ++k) {
+    r.e[2 * k] = from_f32<T>(v[k].x);
+    if (V > 1) r.e[2 * k + 1] = from_f32<T>(v[k].y);
+  }
+  __stcs(reinterpret_cast<typename Raw<T, V>::Q *>(p), r.q);
+}
+template <int V>
+__device__ __forceinline__ float lanes_sum(float2 a) { return V == 1 ? a.x : a.x + a.y; }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// The activations on pairs.  16-bit results take GELU through the paired erf of
+// tc_transforms.cuh (about 2e-6, far below their rounding), fp32 results erff.
+template <typename T>
+__device__ __forceinline__ float2 act_pair(int act, float2 z) {
+  if (act == EQLIN_ACT_SILU) return silu2(z);
+  if (act == EQLIN_ACT_GELU)
+    return sizeof(T) == 2 ? gelu_erf2(z) : make_float2(act_value<EQLIN_ACT_GELU>(z.x), act_value<EQLIN_ACT_GELU>(z.y));
+  return z;
+}
+template <typename T>
+__device__ __forceinline__ float2 slope_pair(int act, float2 z) {
+  float2 a;
+  if (act == EQLIN_ACT_SILU) return silu_slope2(z, a);
+  if (act == EQLIN_ACT_GELU) {
+    if (sizeof(T) == 2) return gelu_slope2(z, a);
+    return make_float2(act_slope<EQLIN_ACT_GELU>(z.x, a.x), act_slope<EQLIN_ACT_GELU>(z.y, a.y));
+  }
+  return both(1.0f);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -84,6 +132,18 @@ template <typename T, int V, int SEG>
 __device__ __forceinline__ void load_affine(const T *p, int c0, int N, float missing, float (&a)[V / SEG]) {
 #pragma unroll
   for (int k = 0; k < V / SEG; ++k) a[k] = p ? to_f32(__ldg(p + (c0 + k * SEG) / N)) : missing;
+}
+template <int V, int SEG>
+__device__ __forceinline__ float2 affine_pair(const float (&a)[V / SEG], int k) {
+  return make_float2(a[2 * k / SEG], a[(V == 1 ? 0 : 2 * k + 1) / SEG]);
+}
+// Sums of a vector's segments, kept as pairs: of a segment's even and odd values
+// (SEG >= 2), or of two segments of one value each.
+template <int V, int SEG> constexpr int seg_pairs() { return SEG >= 2 ? V / SEG : pairs<V>(); }
+template <int SEG> __device__ __forceinline__ constexpr int seg_at(int k) { return SEG >= 2 ? 2 * k / SEG : k; }
+template <int V, int SEG>
+__device__ __forceinline__ float seg_value(const float2 (&s)[seg_pairs<V, SEG>()], int j) {
+  return SEG >= 2 ? s[j].x + s[j].y : (j % 2 ? s[j / 2].y : s[j / 2].x);
 }
 
 // ------------------------------------------------------------ row kernels
@@ -112,12 +172,23 @@ __host__ __device__ inline int row_smem_floats(const GnShape &sh) {
   return (int)(sh.S * sh.L / sh.vec) + 2 * sh.G;
 }
 
+// CTAs per SM that the row kernels' registers are held to (what fits without
+// spilling, by what a lane keeps: its vectors, and gamma, beta and their
+// gradients' sums once per segment).
+template <int V, int SEG, int NV> constexpr int row_ctas_per_sm() {
+  return NV <= 3 ? 8 : NV <= 5 ? (V == SEG ? 8 : V / SEG <= 2 ? 6 : 4) : (V / SEG <= 2 ? 4 : 2);
+}
+template <int V, int SEG, int NV> constexpr int row_backward_ctas_per_sm() {
+  return NV == 1 ? 5 : NV <= 3 ? (V == SEG ? 5 : 3) : NV <= 5 ? (V == SEG ? 4 : 2) : 2;
+}
+
 template <typename T, int V, int SEG, int NV>
-__global__ void __launch_bounds__(32 * kRowWarps)
+__global__ void __launch_bounds__(32 * kRowWarps, row_ctas_per_sm<V, SEG, NV>())
 group_norm_row_kernel(const T *__restrict__ x, const T *__restrict__ gamma, const T *__restrict__ beta,
                       T *__restrict__ y, float *__restrict__ mean_out, float *__restrict__ rstd_out,
                       GnShape sh, float eps, int act) {
   extern __shared__ float row_smem[];
+  constexpr int P = pairs<V>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nv = (int)(sh.S * sh.L / V);
   float *part = row_smem + warp * row_smem_floats(sh);
@@ -136,34 +207,35 @@ group_norm_row_kernel(const T *__restrict__ x, const T *__restrict__ gamma, cons
     load_affine<T, V, SEG>(beta, c * V, sh.N, 0.0f, be[k]);
   }
   for (int64_t b = (int64_t)blockIdx.x * kRowWarps + warp; b < sh.B; b += (int64_t)gridDim.x * kRowWarps) {
-    const T *src = x + b * sh.S * sh.L;
-    float v[NV][V];
+    const T *src = x + b * sh.S * sh.L + lane * V;
+    Raw<T, V> raw[NV];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int q = lane + 32 * k;
-      if (q < nv) {
-        load_vec<T, V>(src + (int64_t)q * V, v[k]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[k][e] = 0.0f;
-      }
-    }
+    for (int k = 0; k < NV; ++k)
+      if (lane + 32 * k < nv) raw[k] = load_raw<T, V>(src + 32 * k * V);
     float m1 = 0.0f, r1 = 0.0f;   // G = 1
     if (sh.G == 1) {
-      float s = 0.0f;
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) s += v[k][e];
-      m1 = warp_sum(s) / n;
-      float ss = 0.0f;
+      float2 s = both(0.0f), ss = both(0.0f);
 #pragma unroll
       for (int k = 0; k < NV; ++k)
         if (lane + 32 * k < nv) {
+          float2 v[P];
+          unpack(raw[k], v);
 #pragma unroll
-          for (int e = 0; e < V; ++e) ss = fmaf(v[k][e] - m1, v[k][e] - m1, ss);
+          for (int e = 0; e < P; ++e) s = add2(s, v[e]);
         }
-      r1 = rsqrtf(warp_sum(ss) / n + eps);
+      m1 = warp_sum(lanes_sum<V>(s)) / n;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (lane + 32 * k < nv) {
+          float2 v[P];
+          unpack(raw[k], v);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const float2 d = add2(v[e], both(-m1));
+            ss = fma2(d, d, ss);
+          }
+        }
+      r1 = rsqrtf(warp_sum(lanes_sum<V>(ss)) / n + eps);
       if (lane == 0) {
         if (mean_out) mean_out[b] = m1;
         if (rstd_out) rstd_out[b] = r1;
@@ -172,10 +244,11 @@ group_norm_row_kernel(const T *__restrict__ x, const T *__restrict__ gamma, cons
 #pragma unroll
       for (int k = 0; k < NV; ++k)
         if (lane + 32 * k < nv) {
-          float s = 0.0f;
+          float2 v[P], s = both(0.0f);
+          unpack(raw[k], v);
 #pragma unroll
-          for (int e = 0; e < V; ++e) s += v[k][e];
-          part[lane + 32 * k] = s;
+          for (int e = 0; e < P; ++e) s = add2(s, v[e]);
+          part[lane + 32 * k] = lanes_sum<V>(s);
         }
       __syncwarp();
       group_sums(part, gmean, sh, lane);
@@ -185,11 +258,15 @@ group_norm_row_kernel(const T *__restrict__ x, const T *__restrict__ gamma, cons
 #pragma unroll
       for (int k = 0; k < NV; ++k)
         if (lane + 32 * k < nv) {
-          const float m = gmean[grp[k]];
-          float s = 0.0f;
+          const float2 m = both(-gmean[grp[k]]);
+          float2 v[P], s = both(0.0f);
+          unpack(raw[k], v);
 #pragma unroll
-          for (int e = 0; e < V; ++e) s = fmaf(v[k][e] - m, v[k][e] - m, s);
-          part[lane + 32 * k] = s;
+          for (int e = 0; e < P; ++e) {
+            const float2 d = add2(v[e], m);
+            s = fma2(d, d, s);
+          }
+          part[lane + 32 * k] = lanes_sum<V>(s);
         }
       __syncwarp();
       group_sums(part, grstd, sh, lane);
@@ -202,17 +279,17 @@ group_norm_row_kernel(const T *__restrict__ x, const T *__restrict__ gamma, cons
       }
       __syncwarp();
     }
-    T *dst = y + b * sh.S * sh.L;
+    T *dst = y + b * sh.S * sh.L + lane * V;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int q = lane + 32 * k;
-      if (q >= nv) continue;
-      const float m = sh.G == 1 ? m1 : gmean[grp[k]], r = sh.G == 1 ? r1 : grstd[grp[k]];
-      float o[V];
+      if (lane + 32 * k >= nv) continue;
+      const float2 m = both(sh.G == 1 ? -m1 : -gmean[grp[k]]), r = both(sh.G == 1 ? r1 : grstd[grp[k]]);
+      float2 v[P];
+      unpack(raw[k], v);
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        o[e] = act_any(act, fmaf((v[k][e] - m) * r, ga[k][e / SEG], be[k][e / SEG]));
-      store_vec<T, V>(dst + (int64_t)q * V, o);
+      for (int e = 0; e < P; ++e)
+        v[e] = act_pair<T>(act, fma2(mul2(add2(v[e], m), r), affine_pair<V, SEG>(ga[k], e), affine_pair<V, SEG>(be[k], e)));
+      store_pairs<T, V>(dst + 32 * k * V, v);
     }
     __syncwarp();   // the next item rewrites part, gmean and grstd
   }
@@ -222,20 +299,21 @@ group_norm_row_kernel(const T *__restrict__ x, const T *__restrict__ gamma, cons
 // segments over the warp's items; at the end the CTA's warps add theirs in
 // turn and the CTA writes one partial per field, part[cta][F][2].
 template <typename T, int V, int SEG, int NV>
-__global__ void __launch_bounds__(32 * kRowWarps)
+__global__ void __launch_bounds__(32 * kRowWarps, row_backward_ctas_per_sm<V, SEG, NV>())
 group_norm_row_backward_kernel(const T *__restrict__ x, const T *__restrict__ dy, const float *__restrict__ mean,
                                const float *__restrict__ rstd, const T *__restrict__ gamma,
                                const T *__restrict__ beta, T *__restrict__ dx, float *__restrict__ part_out,
                                GnShape sh, int act) {
   extern __shared__ float row_smem[];
-  constexpr int NS = V / SEG;
+  constexpr int NS = V / SEG, P = pairs<V>(), SP = seg_pairs<V, SEG>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nv = (int)(sh.S * sh.L / V);
   float *part = row_smem + warp * row_smem_floats(sh);
   float *c1 = part + nv, *c2 = c1 + sh.G;
   const int Lv = sh.L / V, runv = sh.run / V;
   const float inv_n = 1.0f / (float)(sh.S * sh.run);
-  float ga[NV][NS], be[NV][NS], sg[NV][NS], sb[NV][NS];
+  float ga[NV][NS], be[NV][NS];
+  float2 sg[NV][SP], sb[NV][SP];
   int grp[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -245,50 +323,51 @@ group_norm_row_backward_kernel(const T *__restrict__ x, const T *__restrict__ dy
     load_affine<T, V, SEG>(gamma, c * V, sh.N, 1.0f, ga[k]);
     load_affine<T, V, SEG>(beta, c * V, sh.N, 0.0f, be[k]);
 #pragma unroll
-    for (int j = 0; j < NS; ++j) sg[k][j] = sb[k][j] = 0.0f;
+    for (int j = 0; j < SP; ++j) sg[k][j] = sb[k][j] = both(0.0f);
   }
+  // xhat and gamma dz of pair e of vector k (dz too)
+  auto terms = [&](int k, const float2 &v, const float2 &d, float2 m, float2 r, int e, float2 &xh, float2 &dz) {
+    xh = mul2(add2(v, m), r);
+    dz = d;
+    if (act != EQLIN_ACT_NONE)
+      dz = mul2(dz, slope_pair<T>(act, fma2(xh, affine_pair<V, SEG>(ga[k], e), affine_pair<V, SEG>(be[k], e))));
+  };
   for (int64_t b = (int64_t)blockIdx.x * kRowWarps + warp; b < sh.B; b += (int64_t)gridDim.x * kRowWarps) {
-    const int64_t off = b * sh.S * sh.L;
-    // v: x, then xhat; d: dy, then gamma dz
-    float v[NV][V], d[NV][V];
+    const int64_t at = b * sh.S * sh.L + lane * V;
+    Raw<T, V> rx[NV], rd[NV];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int q = lane + 32 * k;
-      if (q < nv) {
-        load_vec<T, V>(x + off + (int64_t)q * V, v[k]);
-        load_vec<T, V>(dy + off + (int64_t)q * V, d[k]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[k][e] = d[k][e] = 0.0f;
+    for (int k = 0; k < NV; ++k)
+      if (lane + 32 * k < nv) {
+        rx[k] = load_raw<T, V>(x + at + 32 * k * V);
+        rd[k] = load_raw<T, V>(dy + at + 32 * k * V);
       }
-    }
-    float s1 = 0.0f, s2 = 0.0f;
-    float r[NV], p2[NV];
+    const float gm = sh.G == 1 ? __ldg(mean + b) : 0.0f, gr = sh.G == 1 ? __ldg(rstd + b) : 0.0f;
+    float s1 = 0.0f, s2 = 0.0f, p2[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int q = lane + 32 * k;
-      r[k] = p2[k] = 0.0f;
+      p2[k] = 0.0f;
       if (q >= nv) continue;
-      const float m = __ldg(mean + b * sh.G + grp[k]);
-      r[k] = __ldg(rstd + b * sh.G + grp[k]);
-      float a1 = 0.0f, a2 = 0.0f;
+      const float2 m = both(sh.G == 1 ? -gm : -__ldg(mean + b * sh.G + grp[k]));
+      const float2 r = both(sh.G == 1 ? gr : __ldg(rstd + b * sh.G + grp[k]));
+      float2 v[P], d[P], a1 = both(0.0f), a2 = both(0.0f);
+      unpack(rx[k], v);
+      unpack(rd[k], d);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xh = (v[k][e] - m) * r[k];
-        float dz = d[k][e];
-        if (act != EQLIN_ACT_NONE) dz *= slope_any(act, fmaf(xh, ga[k][e / SEG], be[k][e / SEG]));
-        sb[k][e / SEG] += dz;
-        sg[k][e / SEG] = fmaf(dz, xh, sg[k][e / SEG]);
-        const float dn = dz * ga[k][e / SEG];
-        a1 += dn;
-        a2 = fmaf(dn, xh, a2);
-        v[k][e] = xh;
-        d[k][e] = dn;
+      for (int e = 0; e < P; ++e) {
+        float2 xh, dz;
+        terms(k, v[e], d[e], m, r, e, xh, dz);
+        sb[k][seg_at<SEG>(e)] = add2(sb[k][seg_at<SEG>(e)], dz);
+        sg[k][seg_at<SEG>(e)] = fma2(dz, xh, sg[k][seg_at<SEG>(e)]);
+        const float2 dn = mul2(dz, affine_pair<V, SEG>(ga[k], e));
+        a1 = add2(a1, dn);
+        a2 = fma2(dn, xh, a2);
       }
-      s1 += a1;
-      s2 += a2;
-      p2[k] = a2;
-      if (sh.G > 1) part[q] = a1;
+      const float l1 = lanes_sum<V>(a1);
+      p2[k] = lanes_sum<V>(a2);
+      s1 += l1;
+      s2 += p2[k];
+      if (sh.G > 1) part[q] = l1;
     }
     if (sh.G == 1) {
       s1 = warp_sum(s1) * inv_n;
@@ -308,11 +387,19 @@ group_norm_row_backward_kernel(const T *__restrict__ x, const T *__restrict__ dy
     for (int k = 0; k < NV; ++k) {
       const int q = lane + 32 * k;
       if (q >= nv) continue;
-      const float m1 = sh.G == 1 ? s1 : c1[grp[k]] * inv_n, m2 = sh.G == 1 ? s2 : c2[grp[k]] * inv_n;
-      float o[V];
+      const float2 m1 = both(sh.G == 1 ? -s1 : -c1[grp[k]] * inv_n), m2 = both(sh.G == 1 ? -s2 : -c2[grp[k]] * inv_n);
+      const float2 m = both(sh.G == 1 ? -gm : -__ldg(mean + b * sh.G + grp[k]));
+      const float2 r = both(sh.G == 1 ? gr : __ldg(rstd + b * sh.G + grp[k]));
+      float2 v[P], d[P];
+      unpack(rx[k], v);
+      unpack(rd[k], d);
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = r[k] * (d[k][e] - m1 - v[k][e] * m2);
-      store_vec<T, V>(dx + off + (int64_t)q * V, o);
+      for (int e = 0; e < P; ++e) {
+        float2 xh, dz;
+        terms(k, v[e], d[e], m, r, e, xh, dz);
+        v[e] = mul2(r, fma2(xh, m2, fma2(dz, affine_pair<V, SEG>(ga[k], e), m1)));
+      }
+      store_pairs<T, V>(dx + at + 32 * k * V, v);
     }
     __syncwarp();
   }
@@ -328,8 +415,9 @@ group_norm_row_backward_kernel(const T *__restrict__ x, const T *__restrict__ dy
         if (q >= nv) continue;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-          seg_b[q * NS + j] = w == 0 ? sb[k][j] : seg_b[q * NS + j] + sb[k][j];
-          seg_g[q * NS + j] = w == 0 ? sg[k][j] : seg_g[q * NS + j] + sg[k][j];
+          const float vb = seg_value<V, SEG>(sb[k], j), vg = seg_value<V, SEG>(sg[k], j);
+          seg_b[q * NS + j] = w == 0 ? vb : seg_b[q * NS + j] + vb;
+          seg_g[q * NS + j] = w == 0 ? vg : seg_g[q * NS + j] + vg;
         }
       }
     }
@@ -377,114 +465,160 @@ __device__ __forceinline__ Stats join(const Stats &a, const Stats &b) {
   Stats r;
   r.n = a.n + b.n;
   if (r.n == 0.0f) return a;
-  const float d = b.mean - a.mean, w = b.n / r.n;
+  const float d = b.mean - a.mean, w = __fdividef(b.n, r.n);
   r.mean = fmaf(d, w, a.mean);
   r.m2 = a.m2 + fmaf(d * d * a.n, w, b.m2);
   return r;
 }
-__device__ __forceinline__ Stats warp_join(Stats a) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+// Over the lanes of aligned teams of `team` lanes (a power of two); the result is
+// the team's first lane's.
+__device__ __forceinline__ Stats team_join(Stats a, int team) {
+  for (int o = 1; o < team; o <<= 1) {
     Stats b;
-    b.n = __shfl_down_sync(0xffffffffu, a.n, o);
-    b.mean = __shfl_down_sync(0xffffffffu, a.mean, o);
-    b.m2 = __shfl_down_sync(0xffffffffu, a.m2, o);
+    b.n = __shfl_down_sync(0xffffffffu, a.n, o, team);
+    b.mean = __shfl_down_sync(0xffffffffu, a.mean, o, team);
+    b.m2 = __shfl_down_sync(0xffffffffu, a.m2, o, team);
     a = join(a, b);
   }
-  return a;   // lane 0
+  return a;
+}
+__device__ __forceinline__ float team_sum(float a, int team) {
+  for (int o = 1; o < team; o <<= 1) a += __shfl_down_sync(0xffffffffu, a, o, team);
+  return a;
+}
+// Lanes per group when a CTA of `threads` joins something for `groups` groups: as
+// many as make one round of it, 1 to 32.
+__device__ __forceinline__ int team_lanes(int groups, int threads) {
+  int t = 32;
+  while (t > 1 && t * groups > threads) t >>= 1;
+  return t;
+}
+
+// A launch's blocks: `first` units of the first pass (items from a0 on) and
+// `second` of the second (items from b0 on), dealt out evenly.  Returns the unit
+// and whether it is of the second pass.
+struct Step {
+  int first, second;
+  int64_t a0, b0;
+};
+__device__ __forceinline__ bool unit_of(const Step &st, int64_t &unit) {
+  const int64_t total = (int64_t)st.first + st.second, i = blockIdx.x;
+  const int64_t k = i * st.first / total;
+  if ((i + 1) * st.first / total > k) {
+    unit = k;
+    return false;
+  }
+  unit = i - k;
+  return true;
+}
+
+constexpr int kAtOnce = 4;   // positions a thread reads together
+
+// Statistics of U vectors `next` values apart, two-pass.
+template <typename T, int V, int U>
+__device__ __forceinline__ Stats block_stats(const T *src, int64_t next) {
+  constexpr int P = pairs<V>();
+  Raw<T, V> raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) raw[u] = load_raw<T, V>(src + u * next);
+  float2 v[U][P], sum = both(0.0f), ss = both(0.0f);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    unpack(raw[u], v[u]);
+#pragma unroll
+    for (int e = 0; e < P; ++e) sum = add2(sum, v[u][e]);
+  }
+  Stats blk;
+  blk.n = (float)(U * V);
+  blk.mean = lanes_sum<V>(sum) * (1.0f / (U * V));   // U V is a power of two
+  const float2 m = both(-blk.mean);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const float2 d = add2(v[u][e], m);
+      ss = fma2(d, d, ss);
+    }
+  blk.m2 = lanes_sum<V>(ss);
+  return blk;
 }
 
 // part[(b chunks + chunk) G + g] = statistics of the chunk's values of group g.
 template <typename T, int V>
-__global__ void __launch_bounds__(kColThreads)
-group_norm_stats_kernel(const T *__restrict__ x, float4 *__restrict__ part, GnShape sh) {
-  extern __shared__ float col_smem[];
+__device__ __forceinline__ void stats_unit(const T *__restrict__ x, float4 *__restrict__ part, const GnShape &sh,
+                                           int64_t b, int chunk, float *smem) {
   const Tiling tl = col_tiling(sh);
-  Stats *ts = reinterpret_cast<Stats *>(col_smem);          // [threads]
-  Stats *gs = ts + tl.threads;                               // [G]
-  const int64_t b = blockIdx.x / sh.chunks;
-  const int chunk = (int)(blockIdx.x % sh.chunks);
+  Stats *ts = reinterpret_cast<Stats *>(smem);   // [threads]
+  Stats *gs = ts + tl.threads;                   // [G]
   const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nwarps = blockDim.x >> 5;
+  const int tid = threadIdx.x;
   const int Lv = sh.L / V, runv = sh.run / V;
   const int pl = tid / tl.tile, col0 = tid % tl.tile;
   for (int g = tid; g < sh.G; g += blockDim.x) gs[g] = Stats{0.0f, 0.0f, 0.0f};
   for (int t = 0; t < tl.tiles; ++t) {
     const int col = t * tl.tile + col0;
-    float mean[V], m2[V], n = 0.0f;
-#pragma unroll
-    for (int e = 0; e < V; ++e) mean[e] = m2[e] = 0.0f;
-    if (pl < tl.lanes && col < Lv) {
-      const T *src = x + b * sh.S * sh.L + (int64_t)col * V;
-#pragma unroll 4
-      for (int64_t s = s0 + pl; s < s1; s += tl.lanes) {
-        float v[V];
-        load_vec<T, V>(src + s * sh.L, v);
-        n += 1.0f;
-        const float inv = __fdividef(1.0f, n);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float d = v[e] - mean[e];
-          mean[e] = fmaf(d, inv, mean[e]);
-          m2[e] = fmaf(d, v[e] - mean[e], m2[e]);
-        }
-      }
-    }
-    // the vector's values belong to one group: one triple per thread
     Stats st{0.0f, 0.0f, 0.0f};
-    if (n > 0.0f) {
-      float mu = 0.0f, ss = 0.0f, sp = 0.0f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) mu += mean[e];
-      mu *= 1.0f / V;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        ss += m2[e];
-        sp = fmaf(mean[e] - mu, mean[e] - mu, sp);
-      }
-      st = Stats{n * V, mu, fmaf(sp, n, ss)};
+    if (pl < tl.lanes && col < Lv) {
+      const T *src = x + (b * sh.S + s0 + pl) * sh.L + (int64_t)col * V;
+      const int64_t next = (int64_t)tl.lanes * sh.L;   // to the thread's next position
+      int left = (int)((s1 - s0 - pl + tl.lanes - 1) / tl.lanes);
+      for (; left >= kAtOnce; left -= kAtOnce, src += kAtOnce * next) st = join(st, block_stats<T, V, kAtOnce>(src, next));
+      for (; left > 0; --left, src += next) st = join(st, block_stats<T, V, 1>(src, next));
     }
     ts[tid] = st;
     __syncthreads();
-    // warp w joins the groups w, w + nwarps, ..: the tile's columns of the group, all position lanes
+    // a team of lanes per group joins the tile's columns of the group, all position lanes
     const int first = t * tl.tile, last = first + tl.tile < Lv ? first + tl.tile : Lv;
-    for (int g = first / runv + warp; g <= (last - 1) / runv; g += nwarps) {
-      const int a = g * runv > first ? g * runv : first;
-      const int z = (g + 1) * runv < last ? (g + 1) * runv : last;
-      const int w = z - a, count = w * tl.lanes;
+    const int g_first = first / runv, groups = (last - 1) / runv - g_first + 1;
+    const int team = team_lanes(groups, blockDim.x), member = tid & (team - 1);
+    for (int k0 = 0; k0 < groups; k0 += blockDim.x / team) {
+      const int k = k0 + tid / team, g = g_first + k;
       Stats acc{0.0f, 0.0f, 0.0f};
-      for (int j = lane; j < count; j += 32) acc = join(acc, ts[(j / w) * tl.tile + a - first + j % w]);
-      acc = warp_join(acc);
-      if (lane == 0) gs[g] = join(gs[g], acc);
+      if (k < groups) {
+        const int a = g * runv > first ? g * runv : first;
+        const int z = (g + 1) * runv < last ? (g + 1) * runv : last;
+        const int w = z - a;
+        for (int l = 0; l < tl.lanes; ++l)
+          for (int j = member; j < w; j += team) acc = join(acc, ts[l * tl.tile + a - first + j]);
+      }
+      acc = team_join(acc, team);
+      if (k < groups && member == 0) gs[g] = join(gs[g], acc);
     }
     __syncthreads();
   }
   for (int g = tid; g < sh.G; g += blockDim.x)
-    part[((int64_t)b * sh.chunks + chunk) * sh.G + g] = make_float4(gs[g].n, gs[g].mean, gs[g].m2, 0.0f);
+    part[(b * sh.chunks + chunk) * sh.G + g] = make_float4(gs[g].n, gs[g].mean, gs[g].m2, 0.0f);
 }
 
 template <typename T, int V, int SEG>
-__global__ void __launch_bounds__(kColThreads)
-group_norm_apply_kernel(const T *__restrict__ x, const T *__restrict__ gamma, const T *__restrict__ beta,
-                        const float4 *__restrict__ part, T *__restrict__ y, float *__restrict__ mean_out,
-                        float *__restrict__ rstd_out, GnShape sh, float eps, int act) {
+__global__ void __launch_bounds__(kColThreads, 2)
+group_norm_step_kernel(const T *__restrict__ x, const T *__restrict__ gamma, const T *__restrict__ beta,
+                       float4 *__restrict__ part, T *__restrict__ y, float *__restrict__ mean_out,
+                       float *__restrict__ rstd_out, GnShape sh, Step step, float eps, int act) {
   extern __shared__ float col_smem[];
+  constexpr int P = pairs<V>();
+  int64_t unit;
+  if (!unit_of(step, unit)) {
+    stats_unit<T, V>(x, part, sh, step.a0 + unit / sh.chunks, (int)(unit % sh.chunks), col_smem);
+    return;
+  }
+  const int64_t b = step.b0 + unit / sh.chunks;
+  const int chunk = (int)(unit % sh.chunks);
   float2 *gs = reinterpret_cast<float2 *>(col_smem);   // [G] mean, rstd
   const Tiling tl = col_tiling(sh);
-  // the last chunks first: what the statistics pass read last is still in L2
-  const int64_t unit = (int64_t)gridDim.x - 1 - blockIdx.x;
-  const int64_t b = unit / sh.chunks;
-  const int chunk = (int)(unit % sh.chunks);
   const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nwarps = blockDim.x >> 5;
-  for (int g = warp; g < sh.G; g += nwarps) {
+  const int tid = threadIdx.x;
+  const int team = team_lanes(sh.G, blockDim.x), member = tid & (team - 1);
+  for (int g0 = 0; g0 < sh.G; g0 += blockDim.x / team) {
+    const int g = g0 + tid / team;
     Stats acc{0.0f, 0.0f, 0.0f};
-    for (int c = lane; c < sh.chunks; c += 32) {
-      const float4 p = __ldg(part + (b * sh.chunks + c) * sh.G + g);
-      acc = join(acc, Stats{p.x, p.y, p.z});
-    }
-    acc = warp_join(acc);
-    if (lane == 0) {
+    if (g < sh.G)
+      for (int c = member; c < sh.chunks; c += team) {
+        const float4 p = part[(b * sh.chunks + c) * sh.G + g];
+        acc = join(acc, Stats{p.x, p.y, p.z});
+      }
+    acc = team_join(acc, team);
+    if (g < sh.G && member == 0) {
       const float r = rsqrtf(acc.m2 / acc.n + eps);
       gs[g] = make_float2(acc.mean, r);
       if (chunk == 0) {
@@ -498,68 +632,96 @@ group_norm_apply_kernel(const T *__restrict__ x, const T *__restrict__ gamma, co
   const int pl = tid / tl.tile;
   if (pl >= tl.lanes) return;
   for (int col = tid % tl.tile; col < Lv; col += tl.tile) {
-    const float2 mr = gs[col / runv];
+    const float2 m = both(-gs[col / runv].x);
     float ga[V / SEG], be[V / SEG];
     load_affine<T, V, SEG>(gamma, col * V, sh.N, 1.0f, ga);
     load_affine<T, V, SEG>(beta, col * V, sh.N, 0.0f, be);
-    const int64_t off = b * sh.S * sh.L + (int64_t)col * V;
-#pragma unroll 4
-    for (int64_t s = s0 + pl; s < s1; s += tl.lanes) {
-      float v[V], o[V];
-      load_vec<T, V>(x + off + s * sh.L, v);
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        o[e] = act_any(act, fmaf((v[e] - mr.x) * mr.y, ga[e / SEG], be[e / SEG]));
-      store_vec<T, V>(y + off + s * sh.L, o);
+    for (int k = 0; k < V / SEG; ++k) ga[k] *= gs[col / runv].y;
+    auto value = [&](const Raw<T, V> &raw, T *dst) {
+      float2 v[P];
+      unpack(raw, v);
+#pragma unroll
+      for (int e = 0; e < P; ++e)
+        v[e] = act_pair<T>(act, fma2(add2(v[e], m), affine_pair<V, SEG>(ga, e), affine_pair<V, SEG>(be, e)));
+      store_pairs<T, V>(dst, v);
+    };
+    const int64_t off = (b * sh.S + s0 + pl) * sh.L + (int64_t)col * V, next = (int64_t)tl.lanes * sh.L;
+    const T *src = x + off;
+    T *dst = y + off;
+    int left = (int)((s1 - s0 - pl + tl.lanes - 1) / tl.lanes);
+    for (; left >= kAtOnce; left -= kAtOnce, src += kAtOnce * next, dst += kAtOnce * next) {
+      Raw<T, V> raw[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) raw[u] = load_last<T, V>(src + u * next);
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) value(raw[u], dst + u * next);
     }
+    for (; left > 0; --left, src += next, dst += next) value(load_last<T, V>(src), dst);
   }
 }
 
-// Backward, pass 1: part[(b chunks + chunk) F + f] = (sum dz, sum dz xhat) of the chunk.
+// Backward, first pass of a chunk: part_f[(b chunks + chunk) F + f] = (sum dz,
+// sum dz xhat), and per group part_g[(b chunks + chunk) G + g] = the same sums
+// weighted with gamma.
 template <typename T, int V, int SEG>
-__global__ void __launch_bounds__(kColThreads)
-group_norm_backward_sums_kernel(const T *__restrict__ x, const T *__restrict__ dy, const float *__restrict__ mean,
-                                const float *__restrict__ rstd, const T *__restrict__ gamma,
-                                const T *__restrict__ beta, float2 *__restrict__ part, GnShape sh, int act) {
-  extern __shared__ float col_smem[];
-  constexpr int NS = V / SEG;
-  float2 *seg = reinterpret_cast<float2 *>(col_smem);   // [lanes][tile NS]
+__device__ __forceinline__ void sums_unit(const T *__restrict__ x, const T *__restrict__ dy,
+                                          const float *__restrict__ mean, const float *__restrict__ rstd,
+                                          const T *__restrict__ gamma, const T *__restrict__ beta,
+                                          float2 *__restrict__ part_f, float2 *__restrict__ part_g,
+                                          const GnShape &sh, int act, int64_t b, int chunk, float *smem) {
+  constexpr int NS = V / SEG, P = pairs<V>(), SP = seg_pairs<V, SEG>();
+  constexpr int kTwo = 2;
+  float2 *seg = reinterpret_cast<float2 *>(smem);   // [lanes][tile NS]
   const Tiling tl = col_tiling(sh);
-  const int64_t b = blockIdx.x / sh.chunks;
-  const int chunk = (int)(blockIdx.x % sh.chunks);
   const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
   const int tid = threadIdx.x;
   const int Lv = sh.L / V, runv = sh.run / V;
   const int pl = tid / tl.tile, col0 = tid % tl.tile;
+  float2 *out_f = part_f + (b * sh.chunks + chunk) * sh.F;
   for (int t = 0; t < tl.tiles; ++t) {
     const int col = t * tl.tile + col0;
-    float sb[NS], sg[NS];
+    float2 sb[SP], sg[SP];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) sb[j] = sg[j] = 0.0f;
+    for (int j = 0; j < SP; ++j) sb[j] = sg[j] = both(0.0f);
     if (pl < tl.lanes && col < Lv) {
-      const float m = __ldg(mean + b * sh.G + col / runv), r = __ldg(rstd + b * sh.G + col / runv);
+      const float2 m = both(-__ldg(mean + b * sh.G + col / runv)), r = both(__ldg(rstd + b * sh.G + col / runv));
       float ga[NS], be[NS];
       load_affine<T, V, SEG>(gamma, col * V, sh.N, 1.0f, ga);
       load_affine<T, V, SEG>(beta, col * V, sh.N, 0.0f, be);
-      const int64_t off = b * sh.S * sh.L + (int64_t)col * V;
-#pragma unroll 2
-      for (int64_t s = s0 + pl; s < s1; s += tl.lanes) {
-        float v[V], d[V];
-        load_vec<T, V>(x + off + s * sh.L, v);
-        load_vec<T, V>(dy + off + s * sh.L, d);
+      auto add = [&](const Raw<T, V> &rx, const Raw<T, V> &rd) {
+        float2 v[P], d[P];
+        unpack(rx, v);
+        unpack(rd, d);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xh = (v[e] - m) * r;
-          float dz = d[e];
-          if (act != EQLIN_ACT_NONE) dz *= slope_any(act, fmaf(xh, ga[e / SEG], be[e / SEG]));
-          sb[e / SEG] += dz;
-          sg[e / SEG] = fmaf(dz, xh, sg[e / SEG]);
+        for (int e = 0; e < P; ++e) {
+          const float2 xh = mul2(add2(v[e], m), r);
+          float2 dz = d[e];
+          if (act != EQLIN_ACT_NONE)
+            dz = mul2(dz, slope_pair<T>(act, fma2(xh, affine_pair<V, SEG>(ga, e), affine_pair<V, SEG>(be, e))));
+          sb[seg_at<SEG>(e)] = add2(sb[seg_at<SEG>(e)], dz);
+          sg[seg_at<SEG>(e)] = fma2(dz, xh, sg[seg_at<SEG>(e)]);
         }
+      };
+      const int64_t off = (b * sh.S + s0 + pl) * sh.L + (int64_t)col * V, next = (int64_t)tl.lanes * sh.L;
+      const T *px = x + off, *pd = dy + off;
+      int left = (int)((s1 - s0 - pl + tl.lanes - 1) / tl.lanes);
+      for (; left >= kTwo; left -= kTwo, px += kTwo * next, pd += kTwo * next) {
+        Raw<T, V> rx[kTwo], rd[kTwo];
+#pragma unroll
+        for (int u = 0; u < kTwo; ++u) {
+          rx[u] = load_raw<T, V>(px + u * next);
+          rd[u] = load_raw<T, V>(pd + u * next);
+        }
+#pragma unroll
+        for (int u = 0; u < kTwo; ++u) add(rx[u], rd[u]);
       }
+      for (; left > 0; --left, px += next, pd += next) add(load_raw<T, V>(px), load_raw<T, V>(pd));
     }
     if (pl < tl.lanes)
 #pragma unroll
-      for (int j = 0; j < NS; ++j) seg[(pl * tl.tile + col0) * NS + j] = make_float2(sb[j], sg[j]);
+      for (int j = 0; j < NS; ++j)
+        seg[(pl * tl.tile + col0) * NS + j] = make_float2(seg_value<V, SEG>(sb, j), seg_value<V, SEG>(sg, j));
     __syncthreads();
     // one thread per field of the tile: its segments, all position lanes
     const int per_field = sh.N / SEG;
@@ -573,60 +735,120 @@ group_norm_backward_sums_kernel(const T *__restrict__ x, const T *__restrict__ d
           a += p.x;
           c += p.y;
         }
-      part[((int64_t)b * sh.chunks + chunk) * sh.F + f0 + f] = make_float2(a, c);
+      out_f[f0 + f] = make_float2(a, c);
     }
-    __syncthreads();
+    __syncthreads();   // the CTA's own global writes are then visible to its threads
   }
-}
-
-// Pass 2, one CTA per item: the chunks' sums in order -> item[b][F] and, with
-// gamma, per group c[b][G] = (sum gamma dz, sum gamma dz xhat) / n.
-template <typename T>
-__global__ void __launch_bounds__(256)
-group_norm_backward_item_kernel(const float2 *__restrict__ part, const T *__restrict__ gamma,
-                                float2 *__restrict__ item, float2 *__restrict__ c, GnShape sh) {
-  const int64_t b = blockIdx.x;
   const int fpg = sh.F / sh.G;
-  const float inv_n = 1.0f / ((float)sh.S * (float)sh.run);
-  for (int f = threadIdx.x; f < sh.F; f += blockDim.x) {
+  const int team = team_lanes(sh.G, blockDim.x), member = tid & (team - 1);
+  for (int g0 = 0; g0 < sh.G; g0 += blockDim.x / team) {
+    const int g = g0 + tid / team;
     float a = 0.0f, q = 0.0f;
-    for (int k = 0; k < sh.chunks; ++k) {
-      const float2 p = __ldg(part + (b * sh.chunks + k) * sh.F + f);
-      a += p.x;
-      q += p.y;
-    }
-    item[b * sh.F + f] = make_float2(a, q);
-  }
-  __syncthreads();   // the CTA's own global writes are visible to its threads
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int g = warp; g < sh.G; g += blockDim.x >> 5) {
-    float a = 0.0f, q = 0.0f;
-    for (int j = lane; j < fpg; j += 32) {
-      const int f = g * fpg + j;
-      const float2 p = item[b * sh.F + f];
-      const float w = gamma ? to_f32(gamma[f]) : 1.0f;
-      a = fmaf(w, p.x, a);
-      q = fmaf(w, p.y, q);
-    }
-    a = warp_sum(a);
-    q = warp_sum(q);
-    if (lane == 0) c[b * sh.G + g] = make_float2(a * inv_n, q * inv_n);
+    if (g < sh.G)
+      for (int j = member; j < fpg; j += team) {
+        const float2 p = out_f[g * fpg + j];
+        const float w = gamma ? to_f32(__ldg(gamma + g * fpg + j)) : 1.0f;
+        a = fmaf(w, p.x, a);
+        q = fmaf(w, p.y, q);
+      }
+    a = team_sum(a, team);
+    q = team_sum(q, team);
+    if (g < sh.G && member == 0) part_g[(b * sh.chunks + chunk) * sh.G + g] = make_float2(a, q);
   }
 }
 
-// dgamma, dbeta from P partials [P][F] of (sum dz, sum dz xhat): 32 fields per
-// CTA, 8 threads per field.
+template <typename T, int V, int SEG>
+__global__ void __launch_bounds__(kColThreads, 2)
+group_norm_backward_step_kernel(const T *__restrict__ x, const T *__restrict__ dy, const float *__restrict__ mean,
+                                const float *__restrict__ rstd, const T *__restrict__ gamma,
+                                const T *__restrict__ beta, float2 *part_f, float2 *part_g, T *__restrict__ dx,
+                                GnShape sh, Step step, int act) {
+  extern __shared__ float col_smem[];
+  constexpr int P = pairs<V>();
+  constexpr int kTwo = 2;
+  int64_t unit;
+  if (!unit_of(step, unit)) {
+    sums_unit<T, V, SEG>(x, dy, mean, rstd, gamma, beta, part_f, part_g, sh, act, step.a0 + unit / sh.chunks,
+                         (int)(unit % sh.chunks), col_smem);
+    return;
+  }
+  const int64_t b = step.b0 + unit / sh.chunks;
+  const int chunk = (int)(unit % sh.chunks);
+  float2 *cs = reinterpret_cast<float2 *>(col_smem);   // [G] the group's two means
+  const Tiling tl = col_tiling(sh);
+  const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
+  const int tid = threadIdx.x;
+  const float inv_n = 1.0f / ((float)sh.S * (float)sh.run);
+  const int team = team_lanes(sh.G, blockDim.x), member = tid & (team - 1);
+  for (int g0 = 0; g0 < sh.G; g0 += blockDim.x / team) {
+    const int g = g0 + tid / team;
+    float a = 0.0f, q = 0.0f;
+    if (g < sh.G)
+      for (int c = member; c < sh.chunks; c += team) {
+        const float2 p = part_g[(b * sh.chunks + c) * sh.G + g];
+        a += p.x;
+        q += p.y;
+      }
+    a = team_sum(a, team);
+    q = team_sum(q, team);
+    if (g < sh.G && member == 0) cs[g] = make_float2(-a * inv_n, -q * inv_n);
+  }
+  __syncthreads();
+  const int Lv = sh.L / V, runv = sh.run / V;
+  const int pl = tid / tl.tile;
+  if (pl >= tl.lanes) return;
+  for (int col = tid % tl.tile; col < Lv; col += tl.tile) {
+    const int g = col / runv;
+    const float2 m = both(-__ldg(mean + b * sh.G + g)), r = both(__ldg(rstd + b * sh.G + g));
+    const float2 m1 = both(cs[g].x), m2 = both(cs[g].y);
+    float ga[V / SEG], be[V / SEG];
+    load_affine<T, V, SEG>(gamma, col * V, sh.N, 1.0f, ga);
+    load_affine<T, V, SEG>(beta, col * V, sh.N, 0.0f, be);
+    auto value = [&](const Raw<T, V> &rx, const Raw<T, V> &rd, T *dst) {
+      float2 v[P], d[P];
+      unpack(rx, v);
+      unpack(rd, d);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const float2 xh = mul2(add2(v[e], m), r);
+        float2 dz = d[e];
+        if (act != EQLIN_ACT_NONE)
+          dz = mul2(dz, slope_pair<T>(act, fma2(xh, affine_pair<V, SEG>(ga, e), affine_pair<V, SEG>(be, e))));
+        v[e] = mul2(r, fma2(xh, m2, fma2(dz, affine_pair<V, SEG>(ga, e), m1)));
+      }
+      store_pairs<T, V>(dst, v);
+    };
+    const int64_t off = (b * sh.S + s0 + pl) * sh.L + (int64_t)col * V, next = (int64_t)tl.lanes * sh.L;
+    const T *px = x + off, *pd = dy + off;
+    T *dst = dx + off;
+    int left = (int)((s1 - s0 - pl + tl.lanes - 1) / tl.lanes);
+    for (; left >= kTwo; left -= kTwo, px += kTwo * next, pd += kTwo * next, dst += kTwo * next) {
+      Raw<T, V> rx[kTwo], rd[kTwo];
+#pragma unroll
+      for (int u = 0; u < kTwo; ++u) {
+        rx[u] = load_last<T, V>(px + u * next);
+        rd[u] = load_last<T, V>(pd + u * next);
+      }
+#pragma unroll
+      for (int u = 0; u < kTwo; ++u) value(rx[u], rd[u], dst + u * next);
+    }
+    for (; left > 0; --left, px += next, pd += next, dst += next) value(load_last<T, V>(px), load_last<T, V>(pd), dst);
+  }
+}
+
+// dgamma, dbeta from R partials [R][F] of (sum dz, sum dz xhat): 16 fields per
+// CTA, 64 threads per field, each a fixed share of the partials.
 template <typename T>
-__global__ void __launch_bounds__(256)
-group_norm_affine_grad_kernel(const float2 *__restrict__ part, int64_t P, int F, T *__restrict__ dgamma,
+__global__ void __launch_bounds__(1024)
+group_norm_affine_grad_kernel(const float2 *__restrict__ part, int64_t R, int F, T *__restrict__ dgamma,
                               T *__restrict__ dbeta) {
-  __shared__ float2 acc[8][32];
-  const int fl = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const int f = blockIdx.x * 32 + fl;
+  __shared__ float2 acc[64][17];
+  const int fl = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int f = blockIdx.x * 16 + fl;
   float a = 0.0f, q = 0.0f;
   if (f < F) {
-#pragma unroll 4
-    for (int64_t p = r; p < P; p += 8) {
+#pragma unroll 8
+    for (int64_t p = r; p < R; p += 64) {
       const float2 v = __ldg(part + p * F + f);
       a += v.x;
       q += v.y;
@@ -634,52 +856,15 @@ group_norm_affine_grad_kernel(const float2 *__restrict__ part, int64_t P, int F,
   }
   acc[r][fl] = make_float2(a, q);
   __syncthreads();
-  if (r == 0 && f < F) {
-    for (int k = 1; k < 8; ++k) {
-      a += acc[k][fl].x;
-      q += acc[k][fl].y;
-    }
-    if (dbeta) dbeta[f] = from_f32<T>(a);
-    if (dgamma) dgamma[f] = from_f32<T>(q);
-  }
-}
-
-// Pass 3: dx.
-template <typename T, int V, int SEG>
-__global__ void __launch_bounds__(kColThreads)
-group_norm_backward_apply_kernel(const T *__restrict__ x, const T *__restrict__ dy, const float *__restrict__ mean,
-                                 const float *__restrict__ rstd, const T *__restrict__ gamma,
-                                 const T *__restrict__ beta, const float2 *__restrict__ c, T *__restrict__ dx,
-                                 GnShape sh, int act) {
-  const Tiling tl = col_tiling(sh);
-  const int64_t unit = (int64_t)gridDim.x - 1 - blockIdx.x;   // as in the forward
-  const int64_t b = unit / sh.chunks;
-  const int chunk = (int)(unit % sh.chunks);
-  const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
-  const int Lv = sh.L / V, runv = sh.run / V;
-  const int pl = threadIdx.x / tl.tile;
-  if (pl >= tl.lanes) return;
-  for (int col = threadIdx.x % tl.tile; col < Lv; col += tl.tile) {
-    const int g = col / runv;
-    const float m = __ldg(mean + b * sh.G + g), r = __ldg(rstd + b * sh.G + g);
-    const float2 cc = __ldg(c + b * sh.G + g);
-    float ga[V / SEG], be[V / SEG];
-    load_affine<T, V, SEG>(gamma, col * V, sh.N, 1.0f, ga);
-    load_affine<T, V, SEG>(beta, col * V, sh.N, 0.0f, be);
-    const int64_t off = b * sh.S * sh.L + (int64_t)col * V;
-#pragma unroll 2
-    for (int64_t s = s0 + pl; s < s1; s += tl.lanes) {
-      float v[V], d[V], o[V];
-      load_vec<T, V>(x + off + s * sh.L, v);
-      load_vec<T, V>(dy + off + s * sh.L, d);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xh = (v[e] - m) * r;
-        float dz = d[e];
-        if (act != EQLIN_ACT_NONE) dz *= slope_any(act, fmaf(xh, ga[e / SEG], be[e / SEG]));
-        o[e] = r * (fmaf(dz, ga[e / SEG], -cc.x) - xh * cc.y);
-      }
-      store_vec<T, V>(dx + off + s * sh.L, o);
+  // warp w < 16 joins field w
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (w < 16) {
+    const float2 u = acc[lane][w], v = acc[lane + 32][w];
+    a = warp_sum(u.x + v.x);
+    q = warp_sum(u.y + v.y);
+    if (lane == 0 && blockIdx.x * 16 + w < F) {
+      if (dbeta) dbeta[blockIdx.x * 16 + w] = from_f32<T>(a);
+      if (dgamma) dgamma[blockIdx.x * 16 + w] = from_f32<T>(q);
     }
   }
 }
@@ -701,10 +886,11 @@ int elem_size(int dtype) { return dtype == EQLIN_F32 ? 4 : 2; }
 // only, since a lane's 8 narrow ones would hold too little to be worth a warp.
 bool row_form(const GnShape &sh) { return sh.S * sh.L / sh.vec <= 32 * kRowVecs; }
 
-constexpr int kRowCtas = 148 * 8;   // CTAs of the row kernels (resident at once; also the partials of dgamma, dbeta)
-constexpr int64_t kChunkTarget = 148 * 6;   // CTAs that the chunk kernels aim at
+constexpr int kRowCtas = 148 * 5;          // CTAs of the backward row kernel (the partials of dgamma, dbeta)
+constexpr int64_t kChunkTarget = 148 * 2;  // CTAs per pass of a launch that the chunk kernels aim at (two fit an SM)
+constexpr int64_t kBatchBytes = 48 << 20;  // of what a batch reads twice: two batches well within L2 (126 MB)
 
-int make_shape(int64_t B, int64_t S, int F, int N, int G, int dtype, GnShape *out) {
+int make_shape(int64_t B, int64_t S, int F, int N, int G, int dtype, int tensors, GnShape *out) {
   if (dtype != EQLIN_F32 && dtype != EQLIN_BF16 && dtype != EQLIN_F16)
     return set_error(EQLIN_ERR_UNSUPPORTED, "dtype %d is not EQLIN_F32, EQLIN_BF16 or EQLIN_F16", dtype);
   if (N < 1 || N > kMaxN) return set_error(EQLIN_ERR_UNSUPPORTED, "N=%d not in 1..16", N);
@@ -722,18 +908,26 @@ int make_shape(int64_t B, int64_t S, int F, int N, int G, int dtype, GnShape *ou
   sh.L = F * N;
   sh.run = sh.L / G;
   if (B > ((int64_t)1 << 40) || S > ((int64_t)1 << 40) || (S > 0 && B > ((int64_t)1 << 46) / S) ||
-      (B > 0 && S > 0 && B * S > ((int64_t)1 << 60) / sh.L))
+      (B > 0 && S > 0 && B * S > ((int64_t)1 << 56) / sh.L))
     return set_error(EQLIN_ERR_UNSUPPORTED, "B=%lld items of S=%lld positions are too many", (long long)B, (long long)S);
   // the widest vector that divides a group's values of a position: it never
   // straddles two groups, and every vector is aligned (the base is)
   sh.vec = gcd(sh.run, 16 / elem_size(dtype));
   sh.chunks = 1;
   sh.per = S;
+  sh.batch = B;
   if (B > 0 && S > 0 && !row_form(sh)) {
-    // at least 4 positions per thread and chunk, so that the joining of a
-    // chunk stays small beside its loads
+    // equal batches of items (up to 5/3 of one stays whole), then chunks of at
+    // least 4 positions per thread, so that the joining of a chunk stays small
+    // beside its loads
+    const int64_t item = S * sh.L * elem_size(dtype) * tensors;
+    sh.batch = kBatchBytes / item;
+    if (sh.batch < 1) sh.batch = 1;
+    if (sh.batch * 5 / 3 >= B) sh.batch = B;
+    const int64_t batches = (B + sh.batch - 1) / sh.batch;
+    sh.batch = (B + batches - 1) / batches;
     const Tiling tl = col_tiling(sh);
-    int64_t want = (kChunkTarget + B - 1) / B;
+    int64_t want = (kChunkTarget + sh.batch - 1) / sh.batch;
     const int64_t most = (S + 4 * tl.lanes - 1) / (4 * tl.lanes);
     if (want > most) want = most;
     if (want < 1) want = 1;
@@ -753,13 +947,13 @@ size_t forward_workspace(const GnShape &sh) {
   return (size_t)sh.B * sh.chunks * sh.G * sizeof(float4);
 }
 
-int64_t row_ctas(const GnShape &sh) {
+int64_t row_ctas(const GnShape &sh, int64_t most = kRowCtas) {
   const int64_t need = (sh.B + kRowWarps - 1) / kRowWarps;
-  return need < kRowCtas ? need : kRowCtas;
+  return need < most ? need : most;
 }
 
 struct BackwardParts {
-  size_t part, item, c, total;   // byte offsets
+  size_t field, group, total;   // byte offsets of the partial sums
 };
 BackwardParts backward_parts(const GnShape &sh) {
   BackwardParts p{};
@@ -768,9 +962,8 @@ BackwardParts backward_parts(const GnShape &sh) {
     p.total = (size_t)row_ctas(sh) * sh.F * sizeof(float2);
     return p;
   }
-  p.item = up16((size_t)sh.B * sh.chunks * sh.F * sizeof(float2));
-  p.c = p.item + up16((size_t)sh.B * sh.F * sizeof(float2));
-  p.total = p.c + (size_t)sh.B * sh.G * sizeof(float2);
+  p.group = up16((size_t)sh.B * sh.chunks * sh.F * sizeof(float2));
+  p.total = p.group + (size_t)sh.B * sh.chunks * sh.G * sizeof(float2);
   return p;
 }
 
@@ -785,19 +978,38 @@ struct Tensors {
 template <typename T, int V, int SEG, int NV>
 int row_forward(const Tensors &t, const GnShape &sh, float eps, int act, cudaStream_t s) {
   const size_t smem = (size_t)kRowWarps * row_smem_floats(sh) * sizeof(float);
-  group_norm_row_kernel<T, V, SEG, NV><<<(unsigned)row_ctas(sh), 32 * kRowWarps, smem, s>>>(
+  group_norm_row_kernel<T, V, SEG, NV><<<(unsigned)row_ctas(sh, 148 * row_ctas_per_sm<V, SEG, NV>()), 32 * kRowWarps, smem, s>>>(
       (const T *)t.x, (const T *)t.gamma, (const T *)t.beta, (T *)t.y, t.mean_out, t.rstd_out, sh, eps, act);
   return check_launch("group norm (rows)");
 }
 
 template <typename T, int V, int SEG, int NV>
-int row_backward(const Tensors &t, const GnShape &sh, int act, float *part, cudaStream_t s) {
+int row_backward(const Tensors &t, const GnShape &sh, int act, float *part, int64_t *ctas, cudaStream_t s) {
   size_t floats = (size_t)kRowWarps * row_smem_floats(sh);
   const size_t segs = 2 * (size_t)(sh.S * sh.L / SEG);
   if (segs > floats) floats = segs;
-  group_norm_row_backward_kernel<T, V, SEG, NV><<<(unsigned)row_ctas(sh), 32 * kRowWarps, floats * sizeof(float), s>>>(
+  *ctas = row_ctas(sh, 148 * row_backward_ctas_per_sm<V, SEG, NV>());
+  group_norm_row_backward_kernel<T, V, SEG, NV><<<(unsigned)*ctas, 32 * kRowWarps, floats * sizeof(float), s>>>(
       (const T *)t.x, (const T *)t.dy, t.mean, t.rstd, (const T *)t.gamma, (const T *)t.beta, (T *)t.y, part, sh, act);
   return check_launch("group norm backward (rows)");
+}
+
+// The launches of the chunk form: step k takes the first pass of batch k and the
+// second of batch k - 1.
+template <class Launch>
+int for_steps(const GnShape &sh, const Launch &launch) {
+  const int64_t batches = (sh.B + sh.batch - 1) / sh.batch;
+  auto units = [&](int64_t k) {
+    if (k < 0 || k >= batches) return (int64_t)0;
+    const int64_t left = sh.B - k * sh.batch;
+    return (left < sh.batch ? left : sh.batch) * sh.chunks;
+  };
+  for (int64_t k = 0; k <= batches; ++k) {
+    const Step st{(int)units(k), (int)units(k - 1), k * sh.batch, (k - 1) * sh.batch};
+    const int rc = launch(st);
+    if (rc) return rc;
+  }
+  return EQLIN_OK;
 }
 
 template <typename T, int V, int SEG>
@@ -810,20 +1022,19 @@ int forward_v(const Tensors &t, const GnShape &sh, float eps, int act, void *ws,
     return row_forward<T, V, SEG, kRowVecs>(t, sh, eps, act, s);
   }
   const Tiling tl = col_tiling(sh);
-  const unsigned grid = (unsigned)(sh.B * sh.chunks);
   float4 *part = static_cast<float4 *>(ws);
-  group_norm_stats_kernel<T, V><<<grid, tl.threads, (tl.threads + sh.G) * sizeof(Stats), s>>>((const T *)t.x, part, sh);
-  int rc = check_launch("group norm (statistics)");
-  if (rc) return rc;
-  group_norm_apply_kernel<T, V, SEG><<<grid, tl.threads, sh.G * sizeof(float2), s>>>(
-      (const T *)t.x, (const T *)t.gamma, (const T *)t.beta, part, (T *)t.y, t.mean_out, t.rstd_out, sh, eps, act);
-  return check_launch("group norm");
+  size_t smem = (tl.threads + sh.G) * sizeof(Stats);
+  return for_steps(sh, [&](const Step &st) {
+    group_norm_step_kernel<T, V, SEG><<<(unsigned)(st.first + st.second), tl.threads, smem, s>>>(
+        (const T *)t.x, (const T *)t.gamma, (const T *)t.beta, part, (T *)t.y, t.mean_out, t.rstd_out, sh, st, eps, act);
+    return check_launch("group norm");
+  });
 }
 
 template <typename T>
 int affine_grad(const Tensors &t, const float2 *part, int64_t P, int F, cudaStream_t s) {
   if (!t.dgamma && !t.dbeta) return EQLIN_OK;
-  group_norm_affine_grad_kernel<T><<<(unsigned)((F + 31) / 32), 256, 0, s>>>(part, P, F, (T *)t.dgamma, (T *)t.dbeta);
+  group_norm_affine_grad_kernel<T><<<(unsigned)((F + 15) / 16), 1024, 0, s>>>(part, P, F, (T *)t.dgamma, (T *)t.dbeta);
   return check_launch("group norm backward (dgamma, dbeta)");
 }
 
@@ -834,51 +1045,46 @@ int backward_v(const Tensors &t, const GnShape &sh, int act, void *ws, cudaStrea
   if (row_form(sh)) {
     const int nv = (int)(sh.S * sh.L / V);
     float *part = t.dgamma || t.dbeta ? reinterpret_cast<float *>(w) : nullptr;
-    rc = nv <= 32    ? row_backward<T, V, SEG, 1>(t, sh, act, part, s)
-         : nv <= 96  ? row_backward<T, V, SEG, 3>(t, sh, act, part, s)
-         : nv <= 160 ? row_backward<T, V, SEG, 5>(t, sh, act, part, s)
-                     : row_backward<T, V, SEG, kRowVecs>(t, sh, act, part, s);
+    int64_t ctas = 0;
+    rc = nv <= 32    ? row_backward<T, V, SEG, 1>(t, sh, act, part, &ctas, s)
+         : nv <= 96  ? row_backward<T, V, SEG, 3>(t, sh, act, part, &ctas, s)
+         : nv <= 160 ? row_backward<T, V, SEG, 5>(t, sh, act, part, &ctas, s)
+                     : row_backward<T, V, SEG, kRowVecs>(t, sh, act, part, &ctas, s);
     if (rc) return rc;
-    return affine_grad<T>(t, reinterpret_cast<const float2 *>(w), row_ctas(sh), sh.F, s);
+    return affine_grad<T>(t, reinterpret_cast<const float2 *>(w), ctas, sh.F, s);
   }
   const BackwardParts p = backward_parts(sh);
   const Tiling tl = col_tiling(sh);
-  const unsigned grid = (unsigned)(sh.B * sh.chunks);
-  float2 *part = reinterpret_cast<float2 *>(w + p.part), *item = reinterpret_cast<float2 *>(w + p.item),
-         *c = reinterpret_cast<float2 *>(w + p.c);
-  group_norm_backward_sums_kernel<T, V, SEG>
-      <<<grid, tl.threads, (size_t)tl.lanes * tl.tile * (V / SEG) * sizeof(float2), s>>>(
-          (const T *)t.x, (const T *)t.dy, t.mean, t.rstd, (const T *)t.gamma, (const T *)t.beta, part, sh, act);
-  if ((rc = check_launch("group norm backward (sums)"))) return rc;
-  group_norm_backward_item_kernel<T><<<(unsigned)sh.B, 256, 0, s>>>(part, (const T *)t.gamma, item, c, sh);
-  if ((rc = check_launch("group norm backward (items)"))) return rc;
-  group_norm_backward_apply_kernel<T, V, SEG><<<grid, tl.threads, 0, s>>>(
-      (const T *)t.x, (const T *)t.dy, t.mean, t.rstd, (const T *)t.gamma, (const T *)t.beta, c, (T *)t.y, sh, act);
-  if ((rc = check_launch("group norm backward"))) return rc;
-  return affine_grad<T>(t, item, sh.B, sh.F, s);
+  float2 *part_f = reinterpret_cast<float2 *>(w + p.field), *part_g = reinterpret_cast<float2 *>(w + p.group);
+  size_t smem = (size_t)tl.lanes * tl.tile * (V / SEG) * sizeof(float2);
+  if (smem < sh.G * sizeof(float2)) smem = sh.G * sizeof(float2);
+  rc = for_steps(sh, [&](const Step &st) {
+    group_norm_backward_step_kernel<T, V, SEG><<<(unsigned)(st.first + st.second), tl.threads, smem, s>>>(
+        (const T *)t.x, (const T *)t.dy, t.mean, t.rstd, (const T *)t.gamma, (const T *)t.beta, part_f, part_g,
+        (T *)t.y, sh, st, act);
+    return check_launch("group norm backward");
+  });
+  if (rc) return rc;
+  return affine_grad<T>(t, part_f, sh.B * sh.chunks, sh.F, s);
 }
 
-// SEG divides N and V: values that share a field.  Full vectors take V or V / 2
-// where it divides N; for odd shapes every value looks up its own field.
-template <typename T, int V>
+// SEG = gcd(N, V): values that share a field.
+template <typename T, int V, int SEG>
 int dispatch_seg(bool backward, const Tensors &t, const GnShape &sh, float eps, int act, void *ws, cudaStream_t s) {
-  if constexpr (V * sizeof(T) == 16) {
-    if (sh.N % V == 0)
-      return backward ? backward_v<T, V, V>(t, sh, act, ws, s) : forward_v<T, V, V>(t, sh, eps, act, ws, s);
-    if (sh.N % (V / 2) == 0)
-      return backward ? backward_v<T, V, V / 2>(t, sh, act, ws, s) : forward_v<T, V, V / 2>(t, sh, eps, act, ws, s);
+  if constexpr (SEG > 1) {
+    if (sh.N % SEG != 0) return dispatch_seg<T, V, SEG / 2>(backward, t, sh, eps, act, ws, s);
   }
-  return backward ? backward_v<T, V, 1>(t, sh, act, ws, s) : forward_v<T, V, 1>(t, sh, eps, act, ws, s);
+  return backward ? backward_v<T, V, SEG>(t, sh, act, ws, s) : forward_v<T, V, SEG>(t, sh, eps, act, ws, s);
 }
 
 template <typename T>
 int dispatch_vec(bool backward, const Tensors &t, const GnShape &sh, float eps, int act, void *ws, cudaStream_t s) {
   if constexpr (sizeof(T) == 2) {
-    if (sh.vec == 8) return dispatch_seg<T, 8>(backward, t, sh, eps, act, ws, s);
+    if (sh.vec == 8) return dispatch_seg<T, 8, 8>(backward, t, sh, eps, act, ws, s);
   }
-  if (sh.vec == 4) return dispatch_seg<T, 4>(backward, t, sh, eps, act, ws, s);
-  if (sh.vec == 2) return dispatch_seg<T, 2>(backward, t, sh, eps, act, ws, s);
-  return dispatch_seg<T, 1>(backward, t, sh, eps, act, ws, s);
+  if (sh.vec == 4) return dispatch_seg<T, 4, 4>(backward, t, sh, eps, act, ws, s);
+  if (sh.vec == 2) return dispatch_seg<T, 2, 2>(backward, t, sh, eps, act, ws, s);
+  return dispatch_seg<T, 1, 1>(backward, t, sh, eps, act, ws, s);
 }
 
 int dispatch(bool backward, int dtype, const Tensors &t, const GnShape &sh, float eps, int act, void *ws,
@@ -912,7 +1118,7 @@ extern "C" {
 
 size_t eqlin_group_norm_workspace_bytes(int64_t B, int64_t S, int F, int N, int G, int dtype) {
   GnShape sh;
-  if (make_shape(B, S, F, N, G, dtype, &sh) != EQLIN_OK) return 0;
+  if (make_shape(B, S, F, N, G, dtype, 1, &sh) != EQLIN_OK) return 0;
   return forward_workspace(sh);
 }
 
@@ -921,7 +1127,7 @@ int eqlin_group_norm(const void *x, const void *gamma, const void *beta, void *y
                      size_t workspace_bytes, eqlin_stream_t stream) {
   clear_error();
   GnShape sh;
-  int rc = make_shape(B, S, F, N, G, dtype, &sh);
+  int rc = make_shape(B, S, F, N, G, dtype, 1, &sh);
   if (rc || (rc = check_act(act))) return rc;
   if (!(eps >= 0.0f)) return set_error(EQLIN_ERR_INVALID_ARG, "eps must be >= 0");
   if (B == 0 || S == 0) return EQLIN_OK;
@@ -942,7 +1148,7 @@ int eqlin_group_norm(const void *x, const void *gamma, const void *beta, void *y
 
 size_t eqlin_group_norm_backward_workspace_bytes(int64_t B, int64_t S, int F, int N, int G, int dtype) {
   GnShape sh;
-  if (make_shape(B, S, F, N, G, dtype, &sh) != EQLIN_OK) return 0;
+  if (make_shape(B, S, F, N, G, dtype, 2, &sh) != EQLIN_OK) return 0;
   return backward_parts(sh).total;
 }
 
@@ -952,7 +1158,7 @@ int eqlin_group_norm_backward(const void *x, const void *dy, const float *mean, 
                               size_t workspace_bytes, eqlin_stream_t stream) {
   clear_error();
   GnShape sh;
-  int rc = make_shape(B, S, F, N, G, dtype, &sh);
+  int rc = make_shape(B, S, F, N, G, dtype, 2, &sh);
   if (rc || (rc = check_act(act))) return rc;
   if (!aligned(dgamma, 16) || !aligned(dbeta, 16))
     return set_error(EQLIN_ERR_ALIGN, "dgamma and dbeta must be 16-byte aligned");

@@ -246,11 +246,18 @@ __host__ __device__ __forceinline__ float2 gelu_tanh2(float2 v) {
 }
 
 // SiLU(v) = v s, s = 1 / (1 + e^-v), and its slope s (1 + v (1 - s)), with the
-// fast exponential and quotient (relative error below 1e-6 where the result is
-// not negligible); `a` receives the value.
+// approximate exponential and reciprocal instructions (relative error below 1e-6
+// where the result is not negligible); `a` receives the value.
 __host__ __device__ __forceinline__ float2 sigmoid2(float2 v) {
 #ifdef __CUDA_ARCH__
-  return make_float2(__fdividef(1.0f, 1.0f + __expf(-v.x)), __fdividef(1.0f, 1.0f + __expf(-v.y)));
+  const float2 t = scl2(v, -1.4426950408889634f);   // e^-v = 2^t
+  float2 e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = add2(e, make_float2(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
+  return s;
 #else
   return make_float2(1.0f / (1.0f + expf(-v.x)), 1.0f / (1.0f + expf(-v.y)));
 #endif
