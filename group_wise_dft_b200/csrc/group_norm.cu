@@ -21,10 +21,11 @@
 //    with one thread per vector of channels (memory order, whole lines), a few
 //    positions at a time: their mean and squared deviations are exact two-pass
 //    sums in registers, joined by the pairwise update of Chan, Golub and LeVeque
-//    (no cancellation, whatever the mean).  A second pass joins the chunks and
-//    normalises.  The items go in batches that fit L2, and one launch takes the
-//    statistics of batch k and normalises batch k - 1, so that the second reading
-//    of x comes from L2 while the first of the next batch comes from memory.
+//    (no cancellation, whatever the mean).  A second launch joins the chunks and
+//    normalises, the last chunks first: they are still in L2.
+// (Batches of items that fit L2, one's first pass in a launch with the previous
+// one's second, were measured and dropped: a batch of 42 MB saves 7 us of memory
+// reads and costs about 20 us of starting and draining a grid.)
 // Statistics, sums and all arithmetic are fp32; every sum has a fixed order.
 #include "activations.cuh"
 #include "eqlin_internal.cuh"
@@ -46,7 +47,6 @@ struct GnShape {
   int vec;          // values per vector
   int chunks;       // per item (chunk kernels)
   int64_t per;      // positions per chunk
-  int64_t batch;    // items per launch
 };
 
 template <int BYTES> struct VecOf;
@@ -494,24 +494,6 @@ __device__ __forceinline__ int team_lanes(int groups, int threads) {
   return t;
 }
 
-// A launch's blocks: `first` units of the first pass (items from a0 on) and
-// `second` of the second (items from b0 on), dealt out evenly.  Returns the unit
-// and whether it is of the second pass.
-struct Step {
-  int first, second;
-  int64_t a0, b0;
-};
-__device__ __forceinline__ bool unit_of(const Step &st, int64_t &unit) {
-  const int64_t total = (int64_t)st.first + st.second, i = blockIdx.x;
-  const int64_t k = i * st.first / total;
-  if ((i + 1) * st.first / total > k) {
-    unit = k;
-    return false;
-  }
-  unit = i - k;
-  return true;
-}
-
 constexpr int kAtOnce = 4;   // positions a thread reads together
 
 // Statistics of U vectors `next` values apart, two-pass.
@@ -545,11 +527,14 @@ __device__ __forceinline__ Stats block_stats(const T *src, int64_t next) {
 
 // part[(b chunks + chunk) G + g] = statistics of the chunk's values of group g.
 template <typename T, int V>
-__device__ __forceinline__ void stats_unit(const T *__restrict__ x, float4 *__restrict__ part, const GnShape &sh,
-                                           int64_t b, int chunk, float *smem) {
+__global__ void __launch_bounds__(kColThreads, 2)
+group_norm_stats_kernel(const T *__restrict__ x, float4 *__restrict__ part, GnShape sh) {
+  extern __shared__ float col_smem[];
+  const int64_t b = blockIdx.x / sh.chunks;
+  const int chunk = (int)(blockIdx.x - b * sh.chunks);
   const Tiling tl = col_tiling(sh);
-  Stats *ts = reinterpret_cast<Stats *>(smem);   // [threads]
-  Stats *gs = ts + tl.threads;                   // [G]
+  Stats *ts = reinterpret_cast<Stats *>(col_smem);   // [threads]
+  Stats *gs = ts + tl.threads;                       // [G]
   const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
   const int tid = threadIdx.x;
   const int Lv = sh.L / V, runv = sh.run / V;
@@ -592,18 +577,14 @@ __device__ __forceinline__ void stats_unit(const T *__restrict__ x, float4 *__re
 
 template <typename T, int V, int SEG>
 __global__ void __launch_bounds__(kColThreads, 2)
-group_norm_step_kernel(const T *__restrict__ x, const T *__restrict__ gamma, const T *__restrict__ beta,
-                       float4 *__restrict__ part, T *__restrict__ y, float *__restrict__ mean_out,
-                       float *__restrict__ rstd_out, GnShape sh, Step step, float eps, int act) {
+group_norm_apply_kernel(const T *__restrict__ x, const T *__restrict__ gamma, const T *__restrict__ beta,
+                        const float4 *__restrict__ part, T *__restrict__ y, float *__restrict__ mean_out,
+                        float *__restrict__ rstd_out, GnShape sh, float eps, int act) {
   extern __shared__ float col_smem[];
   constexpr int P = pairs<V>();
-  int64_t unit;
-  if (!unit_of(step, unit)) {
-    stats_unit<T, V>(x, part, sh, step.a0 + unit / sh.chunks, (int)(unit % sh.chunks), col_smem);
-    return;
-  }
-  const int64_t b = step.b0 + unit / sh.chunks;
-  const int chunk = (int)(unit % sh.chunks);
+  const int64_t unit = (int64_t)gridDim.x - 1 - blockIdx.x;
+  const int64_t b = unit / sh.chunks;
+  const int chunk = (int)(unit - b * sh.chunks);
   float2 *gs = reinterpret_cast<float2 *>(col_smem);   // [G] mean, rstd
   const Tiling tl = col_tiling(sh);
   const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
@@ -665,14 +646,17 @@ group_norm_step_kernel(const T *__restrict__ x, const T *__restrict__ gamma, con
 // sum dz xhat), and per group part_g[(b chunks + chunk) G + g] = the same sums
 // weighted with gamma.
 template <typename T, int V, int SEG>
-__device__ __forceinline__ void sums_unit(const T *__restrict__ x, const T *__restrict__ dy,
-                                          const float *__restrict__ mean, const float *__restrict__ rstd,
-                                          const T *__restrict__ gamma, const T *__restrict__ beta,
-                                          float2 *__restrict__ part_f, float2 *__restrict__ part_g,
-                                          const GnShape &sh, int act, int64_t b, int chunk, float *smem) {
+__global__ void __launch_bounds__(kColThreads, 2)
+group_norm_backward_sums_kernel(const T *__restrict__ x, const T *__restrict__ dy, const float *__restrict__ mean,
+                                const float *__restrict__ rstd, const T *__restrict__ gamma,
+                                const T *__restrict__ beta, float2 *part_f, float2 *__restrict__ part_g, GnShape sh,
+                                int act) {
+  extern __shared__ float col_smem[];
   constexpr int NS = V / SEG, P = pairs<V>(), SP = seg_pairs<V, SEG>();
   constexpr int kTwo = 2;
-  float2 *seg = reinterpret_cast<float2 *>(smem);   // [lanes][tile NS]
+  const int64_t b = blockIdx.x / sh.chunks;
+  const int chunk = (int)(blockIdx.x - b * sh.chunks);
+  float2 *seg = reinterpret_cast<float2 *>(col_smem);   // [lanes][tile NS]
   const Tiling tl = col_tiling(sh);
   const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
   const int tid = threadIdx.x;
@@ -757,23 +741,19 @@ __device__ __forceinline__ void sums_unit(const T *__restrict__ x, const T *__re
   }
 }
 
+// Second pass: dx.
 template <typename T, int V, int SEG>
 __global__ void __launch_bounds__(kColThreads, 2)
-group_norm_backward_step_kernel(const T *__restrict__ x, const T *__restrict__ dy, const float *__restrict__ mean,
-                                const float *__restrict__ rstd, const T *__restrict__ gamma,
-                                const T *__restrict__ beta, float2 *part_f, float2 *part_g, T *__restrict__ dx,
-                                GnShape sh, Step step, int act) {
+group_norm_backward_apply_kernel(const T *__restrict__ x, const T *__restrict__ dy, const float *__restrict__ mean,
+                                 const float *__restrict__ rstd, const T *__restrict__ gamma,
+                                 const T *__restrict__ beta, const float2 *__restrict__ part_g, T *__restrict__ dx,
+                                 GnShape sh, int act) {
   extern __shared__ float col_smem[];
   constexpr int P = pairs<V>();
   constexpr int kTwo = 2;
-  int64_t unit;
-  if (!unit_of(step, unit)) {
-    sums_unit<T, V, SEG>(x, dy, mean, rstd, gamma, beta, part_f, part_g, sh, act, step.a0 + unit / sh.chunks,
-                         (int)(unit % sh.chunks), col_smem);
-    return;
-  }
-  const int64_t b = step.b0 + unit / sh.chunks;
-  const int chunk = (int)(unit % sh.chunks);
+  const int64_t unit = (int64_t)gridDim.x - 1 - blockIdx.x;
+  const int64_t b = unit / sh.chunks;
+  const int chunk = (int)(unit - b * sh.chunks);
   float2 *cs = reinterpret_cast<float2 *>(col_smem);   // [G] the group's two means
   const Tiling tl = col_tiling(sh);
   const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
@@ -887,10 +867,10 @@ int elem_size(int dtype) { return dtype == EQLIN_F32 ? 4 : 2; }
 bool row_form(const GnShape &sh) { return sh.S * sh.L / sh.vec <= 32 * kRowVecs; }
 
 constexpr int kRowCtas = 148 * 5;          // CTAs of the backward row kernel (the partials of dgamma, dbeta)
-constexpr int64_t kChunkTarget = 148 * 2;  // CTAs per pass of a launch that the chunk kernels aim at (two fit an SM)
-constexpr int64_t kBatchBytes = 48 << 20;  // of what a batch reads twice: two batches well within L2 (126 MB)
+constexpr int64_t kChunkResident = 148 * 2;   // CTAs of a chunk kernel that run at once
+constexpr int64_t kChunkFixed = 100 << 10;     // a CTA's start and joins, as bytes of its streaming (about 5 us)
 
-int make_shape(int64_t B, int64_t S, int F, int N, int G, int dtype, int tensors, GnShape *out) {
+int make_shape(int64_t B, int64_t S, int F, int N, int G, int dtype, GnShape *out) {
   if (dtype != EQLIN_F32 && dtype != EQLIN_BF16 && dtype != EQLIN_F16)
     return set_error(EQLIN_ERR_UNSUPPORTED, "dtype %d is not EQLIN_F32, EQLIN_BF16 or EQLIN_F16", dtype);
   if (N < 1 || N > kMaxN) return set_error(EQLIN_ERR_UNSUPPORTED, "N=%d not in 1..16", N);
@@ -915,23 +895,23 @@ int make_shape(int64_t B, int64_t S, int F, int N, int G, int dtype, int tensors
   sh.vec = gcd(sh.run, 16 / elem_size(dtype));
   sh.chunks = 1;
   sh.per = S;
-  sh.batch = B;
   if (B > 0 && S > 0 && !row_form(sh)) {
-    // equal batches of items (up to 5/3 of one stays whole), then chunks of at
-    // least 4 positions per thread, so that the joining of a chunk stays small
-    // beside its loads
-    const int64_t item = S * sh.L * elem_size(dtype) * tensors;
-    sh.batch = kBatchBytes / item;
-    if (sh.batch < 1) sh.batch = 1;
-    if (sh.batch * 5 / 3 >= B) sh.batch = B;
-    const int64_t batches = (B + sh.batch - 1) / sh.batch;
-    sh.batch = (B + batches - 1) / batches;
+    // chunks per item: the fewest rounds of resident CTAs, each as long as its
+    // positions and the fixed part; at least 4 positions per thread
     const Tiling tl = col_tiling(sh);
-    int64_t want = (kChunkTarget + sh.batch - 1) / sh.batch;
-    const int64_t most = (S + 4 * tl.lanes - 1) / (4 * tl.lanes);
-    if (want > most) want = most;
-    if (want < 1) want = 1;
-    sh.per = (S + want - 1) / want;
+    const int64_t most = (S + 4 * tl.lanes - 1) / (4 * tl.lanes), row = (int64_t)sh.L * elem_size(dtype);
+    const int64_t tries = 8 * kChunkResident / B + 1;
+    int64_t best = 1;
+    double least = 0.0;
+    for (int64_t c = 1; c <= most && c <= tries; ++c) {
+      const int64_t rounds = (B * c + kChunkResident - 1) / kChunkResident;
+      const double cost = (double)rounds * ((double)((S + c - 1) / c) * (double)row + (double)kChunkFixed);
+      if (c == 1 || cost < least) {
+        least = cost;
+        best = c;
+      }
+    }
+    sh.per = (S + best - 1) / best;
     sh.chunks = (int)((S + sh.per - 1) / sh.per);
     if (B * sh.chunks > 0x7fffffffLL)
       return set_error(EQLIN_ERR_UNSUPPORTED, "B=%lld items are too many", (long long)B);
@@ -994,24 +974,6 @@ int row_backward(const Tensors &t, const GnShape &sh, int act, float *part, int6
   return check_launch("group norm backward (rows)");
 }
 
-// The launches of the chunk form: step k takes the first pass of batch k and the
-// second of batch k - 1.
-template <class Launch>
-int for_steps(const GnShape &sh, const Launch &launch) {
-  const int64_t batches = (sh.B + sh.batch - 1) / sh.batch;
-  auto units = [&](int64_t k) {
-    if (k < 0 || k >= batches) return (int64_t)0;
-    const int64_t left = sh.B - k * sh.batch;
-    return (left < sh.batch ? left : sh.batch) * sh.chunks;
-  };
-  for (int64_t k = 0; k <= batches; ++k) {
-    const Step st{(int)units(k), (int)units(k - 1), k * sh.batch, (k - 1) * sh.batch};
-    const int rc = launch(st);
-    if (rc) return rc;
-  }
-  return EQLIN_OK;
-}
-
 template <typename T, int V, int SEG>
 int forward_v(const Tensors &t, const GnShape &sh, float eps, int act, void *ws, cudaStream_t s) {
   if (row_form(sh)) {
@@ -1022,13 +984,14 @@ int forward_v(const Tensors &t, const GnShape &sh, float eps, int act, void *ws,
     return row_forward<T, V, SEG, kRowVecs>(t, sh, eps, act, s);
   }
   const Tiling tl = col_tiling(sh);
+  const unsigned grid = (unsigned)(sh.B * sh.chunks);
   float4 *part = static_cast<float4 *>(ws);
-  size_t smem = (tl.threads + sh.G) * sizeof(Stats);
-  return for_steps(sh, [&](const Step &st) {
-    group_norm_step_kernel<T, V, SEG><<<(unsigned)(st.first + st.second), tl.threads, smem, s>>>(
-        (const T *)t.x, (const T *)t.gamma, (const T *)t.beta, part, (T *)t.y, t.mean_out, t.rstd_out, sh, st, eps, act);
-    return check_launch("group norm");
-  });
+  group_norm_stats_kernel<T, V><<<grid, tl.threads, (tl.threads + sh.G) * sizeof(Stats), s>>>((const T *)t.x, part, sh);
+  const int rc = check_launch("group norm (statistics)");
+  if (rc) return rc;
+  group_norm_apply_kernel<T, V, SEG><<<grid, tl.threads, sh.G * sizeof(float2), s>>>(
+      (const T *)t.x, (const T *)t.gamma, (const T *)t.beta, part, (T *)t.y, t.mean_out, t.rstd_out, sh, eps, act);
+  return check_launch("group norm");
 }
 
 template <typename T>
@@ -1056,15 +1019,14 @@ int backward_v(const Tensors &t, const GnShape &sh, int act, void *ws, cudaStrea
   const BackwardParts p = backward_parts(sh);
   const Tiling tl = col_tiling(sh);
   float2 *part_f = reinterpret_cast<float2 *>(w + p.field), *part_g = reinterpret_cast<float2 *>(w + p.group);
-  size_t smem = (size_t)tl.lanes * tl.tile * (V / SEG) * sizeof(float2);
-  if (smem < sh.G * sizeof(float2)) smem = sh.G * sizeof(float2);
-  rc = for_steps(sh, [&](const Step &st) {
-    group_norm_backward_step_kernel<T, V, SEG><<<(unsigned)(st.first + st.second), tl.threads, smem, s>>>(
-        (const T *)t.x, (const T *)t.dy, t.mean, t.rstd, (const T *)t.gamma, (const T *)t.beta, part_f, part_g,
-        (T *)t.y, sh, st, act);
-    return check_launch("group norm backward");
-  });
-  if (rc) return rc;
+  const unsigned grid = (unsigned)(sh.B * sh.chunks);
+  group_norm_backward_sums_kernel<T, V, SEG>
+      <<<grid, tl.threads, (size_t)tl.lanes * tl.tile * (V / SEG) * sizeof(float2), s>>>(
+          (const T *)t.x, (const T *)t.dy, t.mean, t.rstd, (const T *)t.gamma, (const T *)t.beta, part_f, part_g, sh, act);
+  if ((rc = check_launch("group norm backward (sums)"))) return rc;
+  group_norm_backward_apply_kernel<T, V, SEG><<<grid, tl.threads, sh.G * sizeof(float2), s>>>(
+      (const T *)t.x, (const T *)t.dy, t.mean, t.rstd, (const T *)t.gamma, (const T *)t.beta, part_g, (T *)t.y, sh, act);
+  if ((rc = check_launch("group norm backward"))) return rc;
   return affine_grad<T>(t, part_f, sh.B * sh.chunks, sh.F, s);
 }
 
@@ -1118,7 +1080,7 @@ extern "C" {
 
 size_t eqlin_group_norm_workspace_bytes(int64_t B, int64_t S, int F, int N, int G, int dtype) {
   GnShape sh;
-  if (make_shape(B, S, F, N, G, dtype, 1, &sh) != EQLIN_OK) return 0;
+  if (make_shape(B, S, F, N, G, dtype, &sh) != EQLIN_OK) return 0;
   return forward_workspace(sh);
 }
 
@@ -1127,7 +1089,7 @@ int eqlin_group_norm(const void *x, const void *gamma, const void *beta, void *y
                      size_t workspace_bytes, eqlin_stream_t stream) {
   clear_error();
   GnShape sh;
-  int rc = make_shape(B, S, F, N, G, dtype, 1, &sh);
+  int rc = make_shape(B, S, F, N, G, dtype, &sh);
   if (rc || (rc = check_act(act))) return rc;
   if (!(eps >= 0.0f)) return set_error(EQLIN_ERR_INVALID_ARG, "eps must be >= 0");
   if (B == 0 || S == 0) return EQLIN_OK;
@@ -1148,7 +1110,7 @@ int eqlin_group_norm(const void *x, const void *gamma, const void *beta, void *y
 
 size_t eqlin_group_norm_backward_workspace_bytes(int64_t B, int64_t S, int F, int N, int G, int dtype) {
   GnShape sh;
-  if (make_shape(B, S, F, N, G, dtype, 2, &sh) != EQLIN_OK) return 0;
+  if (make_shape(B, S, F, N, G, dtype, &sh) != EQLIN_OK) return 0;
   return backward_parts(sh).total;
 }
 
@@ -1158,7 +1120,7 @@ int eqlin_group_norm_backward(const void *x, const void *dy, const float *mean, 
                               size_t workspace_bytes, eqlin_stream_t stream) {
   clear_error();
   GnShape sh;
-  int rc = make_shape(B, S, F, N, G, dtype, 2, &sh);
+  int rc = make_shape(B, S, F, N, G, dtype, &sh);
   if (rc || (rc = check_act(act))) return rc;
   if (!aligned(dgamma, 16) || !aligned(dbeta, 16))
     return set_error(EQLIN_ERR_ALIGN, "dgamma and dbeta must be 16-byte aligned");
