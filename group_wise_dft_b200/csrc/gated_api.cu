@@ -44,15 +44,9 @@ SpecLayout layout(int N, int F_in, int F_out, size_t tc_bytes) {
 }
 // The fused C_8 kernel where its shapes fit, the two-pass products for the rest
 // of the 16-bit layers.
-#ifndef EQLIN_GEMM8
-#define EQLIN_GEMM8 0
-#endif
-#ifndef EQLIN_GEMMDX
-#define EQLIN_GEMMDX 0
-#endif
 enum Tc { kTcNone, kTcFused, kTcGemm };
 Tc tc_kind(int N, int Cin, int H, int dtype) {
-  if (!EQLIN_GEMM8 && (cyclic_tc_supported(N, Cin, 2 * H, dtype) || cyclic_tc_f16_supported(N, Cin, 2 * H, dtype))) return kTcFused;
+  if (cyclic_tc_supported(N, Cin, 2 * H, dtype) || cyclic_tc_f16_supported(N, Cin, 2 * H, dtype)) return kTcFused;
   return gemm_tc_supported(N, Cin, 2 * H, dtype) && gemm_tc_supported(N, 2 * H, Cin, dtype) ? kTcGemm : kTcNone;
 }
 SpecLayout spec_layout(int N, int Cin, int H, int dtype) {
@@ -60,8 +54,7 @@ SpecLayout spec_layout(int N, int Cin, int H, int dtype) {
   return layout(N, Cin, 2 * H, k == kTcFused ? cyclic_tc_bytes(N, Cin, 2 * H) : k == kTcGemm ? gemm_tc_bytes(N, Cin, 2 * H) : 0);
 }
 SpecLayout adjoint_layout(int N, int Cin, int H, int dtype) {
-  const Tc k = tc_kind(N, Cin, H, dtype);
-  return layout(N, 2 * H, Cin, k == kTcFused && !EQLIN_GEMMDX ? wide_tc_bytes(2 * H, Cin) : k != kTcNone ? gemm_tc_bytes(N, 2 * H, Cin) : 0);
+  return layout(N, 2 * H, Cin, tc_kind(N, Cin, H, dtype) != kTcNone ? gemm_tc_bytes(N, 2 * H, Cin) : 0);
 }
 const float *fp32_section(const void *spec) { return static_cast<const float *>(spec); }
 const void *tc_section(const void *spec, const SpecLayout &L) { return static_cast<const char *>(spec) + L.tc_offset; }
@@ -80,20 +73,29 @@ size_t forward_workspace(int64_t T, int N, int Cin, int H, int dtype) {
   return tc_kind(N, Cin, H, dtype) == kTcGemm ? round256(gemm_tc_spectra_bytes(T, N, Cin)) : 0;
 }
 
+// The backward's workspace.  CUDA cores: dp [T][2H][N] `dtype`, the weight
+// gradient's partials.  Tensor cores: the half spectra of dp and of x, the
+// partials.  Sized for whichever needs more, since the path goes by the call.
 struct BackwardParts {
-  size_t dp, spec, part, total;   // dp [T][2H][N] `dtype`; spectra of x, then of dp; the weight gradient's partials
+  size_t x, part, total;   // (dp, or its spectra, at 0)
 };
-BackwardParts backward_parts(int64_t T, int N, int Cin, int H, int dtype) {
+BackwardParts simt_parts(int64_t T, int N, int Cin, int H, int dtype) {
   BackwardParts p{};
-  p.spec = round256((size_t)T * 2 * H * N * elem_size(dtype));
-  p.part = p.spec;
-  const Tc k = tc_kind(N, Cin, H, dtype);
-  if (k == kTcGemm || (k == kTcFused && EQLIN_GEMMDX)) {
-    const size_t a = gemm_tc_spectra_bytes(T, N, Cin), b = gemm_tc_spectra_bytes(T, N, 2 * H);
-    p.part += round256(a > b ? a : b);
-  }
+  p.part = round256((size_t)T * 2 * H * N * elem_size(dtype));
   p.total = p.part + round256(eqlin_cyclic_weight_grad_workspace_bytes(T, N, Cin, 2 * H, dtype));
   return p;
+}
+BackwardParts tc_parts(int64_t T, int N, int Cin, int H) {
+  BackwardParts p{};
+  p.x = round256(gemm_tc_spectra_bytes(T, N, 2 * H));
+  p.part = p.x + round256(gemm_tc_spectra_bytes(T, N, Cin));
+  p.total = p.part + round256(gemm_tc_wgrad_bytes(T, N, Cin, 2 * H));
+  return p;
+}
+size_t backward_workspace(int64_t T, int N, int Cin, int H, int dtype) {
+  const size_t a = simt_parts(T, N, Cin, H, dtype).total;
+  const size_t b = tc_for(T, N, Cin, H, dtype, EQLIN_PATH_TC) == kTcNone ? 0 : tc_parts(T, N, Cin, H).total;
+  return a > b ? a : b;
 }
 
 int weight_spectrum(const void *W, int N, int Cin, int H, int dtype, bool adjoint, void *out, size_t bytes,
@@ -107,12 +109,9 @@ int weight_spectrum(const void *W, int N, int Cin, int H, int dtype, bool adjoin
   if (bytes < L.total) return set_error(EQLIN_ERR_SIZE, "spectrum buffer of %zu bytes < required %zu", bytes, L.total);
   if (L.tc_bytes) {
     char *tc = static_cast<char *>(out) + L.tc_offset;
-    const Tc k = tc_kind(N, Cin, H, dtype);
-    if (k == kTcGemm || (adjoint && EQLIN_GEMMDX))
-      return adjoint ? launch_gemm_tc_pack(W, N, 2 * H, Cin, true, dtype, out, tc, s)
-                     : launch_gemm_tc_pack(W, N, Cin, 2 * H, false, dtype, out, tc, s);
-    return adjoint ? launch_wide_tc_pack(W, 2 * H, Cin, true, dtype, out, tc, s)
-                   : launch_gated_tc_pack(W, Cin, 2 * H, dtype, out, tc, s);
+    if (adjoint) return launch_gemm_tc_pack(W, N, 2 * H, Cin, true, dtype, out, tc, s);
+    return tc_kind(N, Cin, H, dtype) == kTcFused ? launch_gated_tc_pack(W, Cin, 2 * H, dtype, out, tc, s)
+                                                 : launch_gemm_tc_pack(W, N, Cin, 2 * H, false, dtype, out, tc, s);
   }
   CyclicSpecLayout C{};   // the fp32 section alone
   return adjoint ? launch_cyclic_spectrum(W, N, 2 * H, Cin, dtype, 1, out, C, s)
@@ -198,7 +197,7 @@ size_t eqlin_cyclic_gated_backward_workspace_bytes(int64_t T, int N, int Cin, in
   if (check_shape(N, Cin, H, dtype) != EQLIN_OK || T <= 0 ||
       check_call(T, N, Cin, H, EQLIN_ACT_NONE, EQLIN_PATH_AUTO) != EQLIN_OK)
     return 0;
-  return backward_parts(T, N, Cin, H, dtype).total;
+  return backward_workspace(T, N, Cin, H, dtype);
 }
 
 int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec, const void *Wspec_adj, void *dx,
@@ -220,58 +219,54 @@ int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec
   if (!x || !dh || !Wspec || (dx && !Wspec_adj)) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
   if (!aligned(x, 16) || !aligned(dh, 16) || !aligned(dx, 16) || !aligned(Wspec, 16) || !aligned(Wspec_adj, 16))
     return set_error(EQLIN_ERR_ALIGN, "x, dh, dx and the spectra must be 16-byte aligned");
-  if (path == EQLIN_PATH_TC && tc_kind(N, Cin, H, dtype) == kTcFused && !aligned(dx, 32))
-    return set_error(EQLIN_ERR_ALIGN, "the tensor-core path needs dx 32-byte aligned");
-  const BackwardParts p = backward_parts(T, N, Cin, H, dtype);
+  const size_t need = backward_workspace(T, N, Cin, H, dtype);
   if (!workspace) return set_error(EQLIN_ERR_INVALID_ARG, "null workspace");
-  if (workspace_bytes < p.total)
-    return set_error(EQLIN_ERR_SIZE, "workspace_bytes=%zu < required %zu", workspace_bytes, p.total);
+  if (workspace_bytes < need) return set_error(EQLIN_ERR_SIZE, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
   if (!aligned(workspace, 256)) return set_error(EQLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
   char *ws = static_cast<char *>(workspace);
-  char *dp = ws + p.dp;
-  void *S = ws + p.spec;
   const Tc k = tc_for(T, N, Cin, H, dtype, path);
-  const void *pack = tc_section(Wspec, spec_layout(N, Cin, H, dtype));
-  if (k == kTcFused) {
-    rc = launch_gated_tc(kEpiGates, x, pack, dh, dp, T, Cin, 2 * H, act, dtype, s);
-  } else if (k == kTcGemm) {
-    rc = launch_gemm_tc_spectra(x, S, T, N, Cin, dtype, s);
-    if (!rc) rc = launch_gemm_tc(kEpiGates, S, pack, dh, dp, T, N, Cin, 2 * H, act, dtype, s);
-  } else {
-    GatedIo io{};
-    io.x = x;
-    io.Ws = fp32_section(Wspec);
-    io.dh = dh;
-    io.out = dp;
-    io.T = T;
-    io.Cin = Cin;
-    io.Cout = 2 * H;
-    rc = launch_gated_simt(kEpiGates, io, N, act, dtype, s);
-  }
-  if (rc) return rc;
-  if (dx) {
-    const void *adj = tc_section(Wspec_adj, adjoint_layout(N, Cin, H, dtype));
-    if (k == kTcGemm || (k == kTcFused && EQLIN_GEMMDX)) {
-      rc = launch_gemm_tc_spectra(dp, S, T, N, 2 * H, dtype, s);
-      if (!rc) rc = launch_gemm_tc(kEpiLinear, S, adj, nullptr, dx, T, N, 2 * H, Cin, EQLIN_ACT_NONE, dtype, s);
-    } else if (k == kTcFused && (path == EQLIN_PATH_TC || aligned(dx, 32))) {   // dx in 32-byte pieces
-      rc = launch_wide_tc(dp, adj, dx, T, 2 * H, Cin, dtype, s);
-    } else {
-      GatedIo b{};
-      b.x = dp;
-      b.Ws = fp32_section(Wspec_adj);
-      b.out = dx;
-      b.T = T;
-      b.Cin = 2 * H;
-      b.Cout = Cin;
-      rc = launch_gated_simt(kEpiLinear, b, N, EQLIN_ACT_NONE, dtype, s);
+  if (k != kTcNone) {
+    const BackwardParts p = tc_parts(T, N, Cin, H);
+    void *Sdp = ws, *Sx = ws + p.x;
+    const void *pack = tc_section(Wspec, spec_layout(N, Cin, H, dtype));
+    // the columns past dp's last field are read too
+    if (spectra_width(2 * H) != 2 * H && cudaMemsetAsync(Sdp, 0, p.x, s) != cudaSuccess)
+      return check_launch("gated layer backward (spectra)");
+    if (k == kTcGemm || dW) {
+      if ((rc = launch_gemm_tc_spectra(x, Sx, T, N, Cin, dtype, s))) return rc;
     }
+    rc = k == kTcFused ? launch_gated_tc(kEpiGates, x, pack, dh, Sdp, T, Cin, 2 * H, act, dtype, s)
+                       : launch_gemm_tc(kEpiGates, Sx, pack, dh, Sdp, T, N, Cin, 2 * H, act, dtype, s);
+    if (!rc && dx)
+      rc = launch_gemm_tc(kEpiLinear, Sdp, tc_section(Wspec_adj, adjoint_layout(N, Cin, H, dtype)), nullptr, dx, T, N,
+                          2 * H, Cin, EQLIN_ACT_NONE, dtype, s);
+    if (!rc && dW)
+      rc = launch_gemm_tc_wgrad(Sx, Sdp, dW, T, N, Cin, 2 * H, dtype, reinterpret_cast<float *>(ws + p.part), s);
+    return rc;
   }
-  if (rc) return rc;
+  const BackwardParts p = simt_parts(T, N, Cin, H, dtype);
+  GatedIo io{};
+  io.x = x;
+  io.Ws = fp32_section(Wspec);
+  io.dh = dh;
+  io.out = ws;
+  io.T = T;
+  io.Cin = Cin;
+  io.Cout = 2 * H;
+  if ((rc = launch_gated_simt(kEpiGates, io, N, act, dtype, s))) return rc;
+  if (dx) {
+    GatedIo b{};
+    b.x = ws;
+    b.Ws = fp32_section(Wspec_adj);
+    b.out = dx;
+    b.T = T;
+    b.Cin = 2 * H;
+    b.Cout = Cin;
+    if ((rc = launch_gated_simt(kEpiLinear, b, N, EQLIN_ACT_NONE, dtype, s))) return rc;
+  }
   if (!dW) return EQLIN_OK;
-  return eqlin_cyclic_weight_grad_ex(x, dp, dW, T, N, Cin, 2 * H, dtype, ws + p.part,
-                                     workspace_bytes - p.part,
-                                     path == EQLIN_PATH_SIMT ? EQLIN_PATH_SIMT : EQLIN_PATH_AUTO, stream);
+  return eqlin_cyclic_weight_grad_ex(x, ws, dW, T, N, Cin, 2 * H, dtype, ws + p.part, workspace_bytes - p.part,
+                                     EQLIN_PATH_SIMT, stream);
 }
 
 }  // extern "C"

@@ -17,7 +17,7 @@
 // bytes per CTA), both by TMA with the 128-byte swizzle, all signalling the
 // leader's barrier of the ring slot.  Warps: producer (one thread), MMA issuer
 // (leader), 12 epilogue warps (TMEM -> inverse DFT -> activation and product ->
-// global).  Where two units' accumulators fit TMEM, one unit's epilogue runs
+// global; or the gates' gradients -> DFT -> their half spectra).  Where two units' accumulators fit TMEM, one unit's epilogue runs
 // under the next one's products.
 // The spectra cost a pass over x that the fused C_8 kernel does not have, but
 // nothing is transformed twice and no transform sits between a load and its MMA:
@@ -86,16 +86,13 @@ __host__ __device__ inline int64_t weight_row(const Groups &gr, int F_in, int N,
   const int64_t per = (int64_t)k_blocks(F_in) * num_stages(N) * 2;
   return per * gr.first(g) + (int64_t)((kb * num_stages(N) + st) * 2 + half) * gr.co(g);
 }
-// Width of S's rows: a multiple of 8 values (16 bytes), at least one box.
-__host__ __device__ inline int padded(int F) { return F < kK ? kK : (F + 7) / 8 * 8; }
-
 // ---------------------------------------------------------------- pre-pass
 
-// x [T][F][N] -> S[c][t][padded F], one thread per (token, two fields).
+// x [T][F][N] -> S[c][t][spectra_width(F)], one thread per (token, two fields).
 template <int N, typename T, bool H>
 __global__ void __launch_bounds__(256)
 spectra_kernel(const T *__restrict__ x, uint32_t *__restrict__ S, int64_t Tn, int F, Trig trig) {
-  const int half = padded(F) / 2;
+  const int half = spectra_width(F) / 2;
   const int64_t n = Tn * half;
   for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < n; p += (int64_t)gridDim.x * 256) {
     const int64_t t = p / half;
@@ -236,20 +233,20 @@ __device__ __forceinline__ void gemm_epilogue(uint32_t tb, int half, int64_t tok
           if (args.act == EQLIN_ACT_GELU) slope = gelu_slope2(g, a);
           const float2 dd = make_float2(d[s], d[e]);
           const float2 dg = mul2(mul2(dd, u), slope), du = mul2(dd, a);
-          p[s] = make_float2(dg.x, du.x);
           p[e] = make_float2(dg.y, du.y);
+          p[s] = make_float2(dg.x, du.x);
         }
       }
       if constexpr (EPI == kEpiGated) {
         store_field<N, T>(out + at, d);
       } else {
-        float y[N];
+        // dp leaves as its half spectra
+        fwd_dft2<N>(p, z, args.trig);
+        const int width = spectra_width(F_out);
+        uint16_t *dst = static_cast<uint16_t *>(args.out) + (size_t)tok * width + f;
 #pragma unroll
-        for (int s = 0; s < N; ++s) y[s] = p[s].x;
-        store_field<N, T>(out + 2 * at, y);
-#pragma unroll
-        for (int s = 0; s < N; ++s) y[s] = p[s].y;
-        store_field<N, T>(out + 2 * at + N, y);
+        for (int c = 0; c < N; ++c)
+          *reinterpret_cast<uint32_t *>(dst + (size_t)c * args.T * width) = pack_x2<H>(z[c].x, z[c].y);
       }
     }
   }
@@ -520,7 +517,7 @@ int launch_gemm(const void *S, const void *pack, const void *dh, void *out, int6
   const Groups gr(F_out, N);
   const int co_big = gr.co(0), co_small = gr.co(gr.n - 1);
   CUtensorMap ms, mb, mt;
-  int rc = tma_map_2d_bf16(&ms, S, (uint64_t)padded(F_in), (uint64_t)T * N, (uint64_t)padded(F_in) * 2, kK, kRows, true);
+  int rc = tma_map_2d_bf16(&ms, S, (uint64_t)spectra_width(F_in), (uint64_t)T * N, (uint64_t)spectra_width(F_in) * 2, kK, kRows, true);
   if (rc) return rc;
   const uint64_t rows = (uint64_t)weight_row(gr, F_in, N, gr.n - 1, k_blocks(F_in), 0, 0);
   rc = tma_map_2d_bf16(&mb, pack, kK, rows, 128, kK, (uint32_t)co_big, true);
@@ -557,7 +554,7 @@ int launch_gemm(const void *S, const void *pack, const void *dh, void *out, int6
 
 template <int N, typename T, bool H>
 int launch_spectra(const void *x, void *S, int64_t Tn, int F, cudaStream_t s) {
-  const int64_t n = Tn * (padded(F) / 2), want = (n + 255) / 256;
+  const int64_t n = Tn * (spectra_width(F) / 2), want = (n + 255) / 256;
   const unsigned grid = (unsigned)(want < 148 * 16 ? want : 148 * 16);
   spectra_kernel<N, T, H><<<grid, 256, 0, s>>>(static_cast<const T *>(x), static_cast<uint32_t *>(S), Tn, F, make_trig(N));
   return check_launch("half spectra");
@@ -589,7 +586,7 @@ size_t gemm_tc_bytes(int N, int F_in, int F_out) {
   return (size_t)weight_row(gr, F_in, N, gr.n - 1, k_blocks(F_in), 0, 0) * 128;
 }
 
-size_t gemm_tc_spectra_bytes(int64_t T, int N, int F) { return (size_t)T * N * padded(F) * 2; }
+size_t gemm_tc_spectra_bytes(int64_t T, int N, int F) { return (size_t)T * N * spectra_width(F) * 2; }
 
 bool gemm_tc_tokens_ok(int64_t T, int N, int F_out) {
   return T <= (int64_t)0x7fff0000LL / N && T <= (int64_t)0x7fff0000LL / Groups(F_out, N).n;

@@ -8,7 +8,12 @@ namespace eqlin {
 // What a pass of the spectral product kernels does with its outputs.
 constexpr int kEpiLinear = 0;   // y[t][o] = p[t][o]
 constexpr int kEpiGated = 1;    // h[t][j] = act(p[t][2j]) p[t][2j + 1]
-constexpr int kEpiGates = 2;    // from dh[t][j]: dp[t][2j] = dh p[t][2j + 1] act'(p[t][2j]), dp[t][2j + 1] = dh act(p[t][2j])
+constexpr int kEpiGates = 2;    // from dh[t][j]: dp[t][2j] = dh p[t][2j + 1] act'(p[t][2j]), dp[t][2j + 1] = dh act(p[t][2j]);
+                                // the tensor-core kernels write dp's half spectra
+
+// Half spectra as matrices S[c][t][field] (c in DftTables' order): the width of a
+// row, a multiple of 8 values (16 bytes) and at least one 64-field box.
+__host__ __device__ inline int spectra_width(int F) { return F < 64 ? 64 : (F + 7) / 8 * 8; }
 
 struct GatedIo {
   const void *x;      // [T][Cin][N]
@@ -43,20 +48,9 @@ int launch_gated_tc_pack(const void *W, int Cin, int Cout, int dtype, void *Ws, 
 int launch_gated_tc(int epi, const void *x, const void *Bpack, const void *dh, void *out, int64_t T, int Cin,
                     int Cout, int act, int dtype, cudaStream_t s);
 
-// C_8 layer with any number of input fields on tensor cores (gated_wide_tc.cu),
-// bf16 and fp16: y[T][F_out][8] from x[T][F_in][8], F_in a multiple of 16, F_out
-// of 8.  The pack (wide_tc_bytes) is W [F_out][F_in][8]'s, or with adjoint that
-// of V[o][i][m] = W[i][o][-m], W [F_in][F_out][8]; Ws: the fp32 spectrum beside it.
-bool wide_tc_supported(int N, int F_in, int F_out, int dtype);
-size_t wide_tc_bytes(int F_in, int F_out);
-int launch_wide_tc_pack(const void *W, int F_in, int F_out, bool adjoint, int dtype, void *Ws, void *dst,
-                        cudaStream_t s);
-int launch_wide_tc(const void *x, const void *pack, void *y, int64_t T, int F_in, int F_out, int dtype,
-                   cudaStream_t s);
-
 // Any N on tensor cores (gated_gemm_tc.cu), bf16 and fp16, at least 16 input
 // fields: the half spectra S of x [T][F][N] (gemm_tc_spectra_bytes, 256-byte
-// aligned), then the products with the packed weights (gemm_tc_bytes) of the layer
+// aligned; columns past F zero), then the products with the packed weights (gemm_tc_bytes) of the layer
 // F_in -> F_out and epilogue `epi`.  The pack is W [F_out][F_in][N]'s or, with
 // adjoint, that of V[o][i][m] = W[i][o][-m]; Ws: the fp32 spectrum beside it.
 bool gemm_tc_supported(int N, int F_in, int F_out, int dtype);
@@ -68,5 +62,12 @@ int launch_gemm_tc_pack(const void *W, int N, int F_in, int F_out, bool adjoint,
                         cudaStream_t s);
 int launch_gemm_tc(int epi, const void *S, const void *pack, const void *dh, void *out, int64_t T, int N, int F_in,
                    int F_out, int act, int dtype, cudaStream_t s);
+
+// Weight gradient from half spectra (gated_wgrad_tc.cu), any N, bf16 and fp16:
+// dW[o][i][m] = sum_t sum_g dp[t][o][g] x[t][i][g - m] from S of x (F_in fields) and
+// of dp (F_out fields); part: gemm_tc_wgrad_bytes of fp32 partials.
+size_t gemm_tc_wgrad_bytes(int64_t T, int N, int F_in, int F_out);
+int launch_gemm_tc_wgrad(const void *Sx, const void *Sdp, void *dW, int64_t T, int N, int F_in, int F_out, int dtype,
+                         float *part, cudaStream_t s);
 
 }  // namespace eqlin

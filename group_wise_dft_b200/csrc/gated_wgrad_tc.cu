@@ -1,0 +1,433 @@
+// Weight gradient of a cyclic layer from half spectra, on tcgen05 tensor cores,
+// any N, bf16 or fp16 (the gated layer's backward pass).
+//
+// dW[o,i,m] = sum_t sum_g dp[t,o,g] x[t,i,(g-m) mod N] is a product per bin summed
+// over tokens, C_k[o,i] = sum_t D_k[t,o] conj(X_k[t,i]):
+//     real bins:    C = sum D X,
+//     complex bins: Re C = sum (Dr Xr + Di Xi),  Im C = sum (Di Xr - Dr Xi),
+// with the spectra D, X already in memory as S[c][t][field] (the data gradient
+// reads the same D).  Per coordinate that is a GEMM over tokens whose operands lie
+// with the fields contiguous: both are MN-major for the MMA, no transposition.
+//
+// A work unit is (token split, bin, tile of 256 outputs, tile of up to 256 inputs)
+// on a CTA pair (cta_group::2, M = 256: 128 outputs per CTA; each CTA brings half
+// of the tile's inputs as B): both coordinates' accumulators in TMEM (2 ni <= 512
+// columns).  Stages of 64 tokens: A 2 coordinates x 2 boxes of 64 fields, B 2 x
+// ceil(ni / 128) boxes, by TMA with the 128-byte swizzle and zero fill past the last
+// token or field, all signalling the leader.  Splits write fp32 partials
+// [split][c][o][i]; a second kernel adds them in order and inverts the DFT.
+// Bound by the operands' way from L2: a stage's 48 to 64 KB per CTA feed 4 to 16 MMAs.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "dft_pairs.cuh"
+#include "gated_internal.cuh"
+#include "tc_host.h"
+#include "tc_primitives.cuh"
+
+namespace eqlin {
+namespace {
+
+constexpr int kProd = 0;          // TMA producer; TMEM allocation
+constexpr int kMma = 1;           // MMA issuer (leader)
+constexpr int kEpi0 = 2;
+constexpr int kNumEpi = 12;       // three per TMEM lane quarter
+constexpr int kThreads = 32 * (kEpi0 + kNumEpi);
+constexpr int kTok = 64;                       // tokens per stage
+constexpr int kBox = kTok * 128;               // 64 fields of one coordinate
+constexpr int kMaxSlots = 4;
+constexpr int kCtrl = 256;
+constexpr int kSmemLimit = 232448;
+constexpr int kOTile = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kSleep = 64;
+constexpr int kPairs = 74;
+
+struct Plan {
+  int bins, n_ot, n_it, ni;     // ni: inputs per tile (a multiple of 32)
+  int splits, stages;           // stages of 64 tokens per split
+};
+
+Plan plan_for(int64_t T, int N, int F_in, int F_out) {
+  Plan p;
+  p.bins = 1 + (N - 1) / 2;
+  p.n_ot = (F_out + kOTile - 1) / kOTile;
+  p.n_it = (F_in + 255) / 256;
+  p.ni = ((F_in + p.n_it - 1) / p.n_it + 31) / 32 * 32;
+  const int64_t total = (T + kTok - 1) / kTok, per = (int64_t)p.bins * p.n_ot * p.n_it;
+  // splits: the fewest rounds of CTA pairs, each as long as its stages and a
+  // fixed part (filling the ring, draining the accumulators) of about 8
+  int64_t best = 1, least = -1;
+  for (int64_t s = 1; s <= 64 && s <= (total + 3) / 4; ++s) {
+    const int64_t rounds = (per * s + kPairs - 1) / kPairs, cost = rounds * ((total + s - 1) / s + 8);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  p.stages = (int)((total + best - 1) / best);
+  p.splits = (int)((total + p.stages - 1) / p.stages);
+  return p;
+}
+
+struct WgArgs {
+  float *part;
+  unsigned int *fault;
+  unsigned int epoch;
+  int64_t T;
+  int N, F_in, F_out, units, nslots, slot_bytes;
+  Plan plan;
+};
+
+template <bool H>
+__global__ void __launch_bounds__(kThreads, 1)
+    spectral_wgrad_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant__ CUtensorMap map_x,
+                          const __grid_constant__ WgArgs args) {
+  using namespace tc;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *const gbase = smem_raw + (base - raw);
+  const int nslots = args.nslots;
+  const uint32_t slot_bytes = (uint32_t)args.slot_bytes;
+  const uint32_t sBar = base + (uint32_t)nslots * slot_bytes;
+  auto bar_full = [&](int s) { return sBar + 8u * s; };                  // both CTAs' stage landed (leader)
+  auto bar_empty = [&](int s) { return sBar + 8u * (kMaxSlots + s); };   // the slot's MMAs are done
+  const uint32_t bar_acc_full = sBar + 8u * (2 * kMaxSlots);
+  const uint32_t bar_acc_empty = sBar + 8u * (2 * kMaxSlots + 1);        // leader
+  const uint32_t tmem_slot = sBar + 8u * (2 * kMaxSlots + 2);
+  static_assert(8 * (2 * kMaxSlots + 2) + 4 <= kCtrl, "control block");
+  volatile uint32_t *tmem_slot_ptr = reinterpret_cast<volatile uint32_t *>(gbase + (tmem_slot - base));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const FaultCtx fault{args.fault, args.epoch};
+  const Plan &pl = args.plan;
+  const int N = args.N;
+  const bool mid = N > 1 && N % 2 == 0;
+  const int nbx = (pl.ni / 2 + 63) / 64;            // boxes of B per coordinate and CTA
+  const uint32_t a_coord = 2u * kBox, b_coord = (uint32_t)nbx * kBox;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    mbar_init(bar_acc_full, 1);
+    mbar_init(bar_acc_empty, 2 * kNumEpi);
+    fence_mbarrier_init_cluster();
+  }
+  if (warp == kProd) tmem_alloc_pair(tmem_slot, kTmemCols);
+  tcgen05_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tcgen05_fence_after();
+  const uint32_t tmem_base = *tmem_slot_ptr;
+
+  // unit u = ((split bins + bin) n_ot + ot) n_it + it
+  struct Unit {
+    int split, bin, ot, it, stages;
+  };
+  const int total_stages = (int)((args.T + kTok - 1) / kTok);
+  const int nunits = args.units > pair ? (args.units - pair + npairs - 1) / npairs : 0;
+  auto unit_at = [&](int n) {
+    int u = pair + n * npairs;
+    Unit r;
+    r.it = u % pl.n_it;
+    u /= pl.n_it;
+    r.ot = u % pl.n_ot;
+    u /= pl.n_ot;
+    r.bin = u % pl.bins;
+    r.split = u / pl.bins;
+    const int left = total_stages - r.split * pl.stages;
+    r.stages = left < pl.stages ? left : pl.stages;
+    return r;
+  };
+  // coordinates of bin b: b = 0 the real bins 0 and N / 2 (if N is even), else Re, Im
+  auto two_of = [&](int bin) { return bin > 0 || mid; };
+
+  if (warp == kProd) {
+    if (elect_one_sync()) {
+      prefetch_tensormap(&map_d);
+      prefetch_tensormap(&map_x);
+      const uint32_t leader_full = mapa_shared(bar_full(0), 0);
+      uint32_t s = 0, ph = 0;
+      bool ok = true;
+      for (int n = 0; n < nunits && ok; ++n) {
+        const Unit u = unit_at(n);
+        const int nc = two_of(u.bin) ? 2 : 1;
+        const int o0 = u.ot * kOTile + (int)rank * 128, i0 = u.it * pl.ni + (int)rank * (pl.ni / 2);
+        const uint32_t bytes = (uint32_t)nc * (a_coord + b_coord);
+        int t = u.split * pl.stages * kTok;
+        for (int st = 0; st < u.stages; ++st, t += kTok) {
+          if (!mbar_wait_bounded(bar_empty(s), ph ^ 1u, fault, FAULT_WAIT_B_EMPTY, kWaitNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t slot = base + s * slot_bytes, full = leader_full + 8u * s;
+          if (leader) mbar_arrive_expect_tx(bar_full(s), 2u * bytes);
+          for (int k = 0; k < nc; ++k) {
+            const int c = u.bin == 0 ? (k == 0 ? 0 : N - 1) : 2 * u.bin - 1 + k;
+            for (int b = 0; b < 2; ++b)
+              tma_load_3d_pair(slot + (uint32_t)k * a_coord + (uint32_t)b * kBox, &map_d, full, o0 + 64 * b, t, c);
+            for (int b = 0; b < nbx; ++b)
+              tma_load_3d_pair(slot + 2u * a_coord + (uint32_t)k * b_coord + (uint32_t)b * kBox, &map_x, full,
+                               i0 + 64 * b, t, c);
+          }
+          if (++s == (uint32_t)nslots) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMma) {
+    if (leader) {
+      const uint64_t d0 = smem_desc_mnmajor_sw128(base, (uint32_t)kBox);
+      const uint32_t d_lo = (uint32_t)d0, d_hi = (uint32_t)(d0 >> 32);
+      const uint32_t id = (H ? idesc_f16_f32(256, pl.ni) : idesc_bf16_f32(256, pl.ni)) | kIdescMnMajor;
+      uint32_t s = 0, ph = 0;
+      bool ok = true;
+      for (int n = 0; n < nunits && ok; ++n) {
+        const Unit u = unit_at(n);
+        const bool two = two_of(u.bin);
+        if (!mbar_wait_bounded_warp(bar_acc_empty, ((uint32_t)n & 1u) ^ 1u, fault, FAULT_WAIT_ACC_EMPTY, kWaitNs)) {
+          ok = false;
+          break;
+        }
+        tcgen05_fence_after();
+        for (int st = 0; st < u.stages; ++st) {
+          if (!mbar_wait_bounded_warp(bar_full(s), ph, fault, FAULT_WAIT_A_FULL, kWaitNs)) {
+            ok = false;
+            break;
+          }
+          tcgen05_fence_after();
+          if (elect_one_sync()) {
+#pragma unroll
+            for (int k = 0; k < kTok / 16; ++k) {
+              const uint32_t acc = st > 0 || k > 0 ? 1u : 0u;
+              // a K-step of 16 tokens: two 8-token groups of 1024 bytes
+              const uint32_t a_re = d_lo + s * (slot_bytes >> 4) + (uint32_t)k * (2048u >> 4);
+              const uint32_t a_im = a_re + (a_coord >> 4), b_re = a_re + (2u * a_coord >> 4), b_im = b_re + (b_coord >> 4);
+              const uint32_t c_re = tmem_base, c_im = tmem_base + (uint32_t)pl.ni;
+              mma_bf16_pair_w(c_re, a_re, d_hi, b_re, d_hi, id, acc);
+              if (u.bin == 0) {
+                if (two) mma_bf16_pair_w(c_im, a_im, d_hi, b_im, d_hi, id, acc);
+              } else {
+                mma_bf16_pair_w(c_re, a_im, d_hi, b_im, d_hi, id, 1u);
+                mma_bf16_pair_w(c_im, a_im, d_hi, b_re, d_hi, id, acc);
+                mma_bf16_pair_w(c_im, a_re, d_hi, b_im, d_hi, id | (1u << 14), 1u);
+              }
+            }
+            mma_commit_pair_mc(bar_empty(s), 0x3);
+          }
+          __syncwarp();
+          if (++s == (uint32_t)nslots) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (elect_one_sync()) mma_commit_pair_mc(bar_acc_full, 0x3);
+        __syncwarp();
+      }
+    }
+  } else {
+    // TMEM lane = output of this CTA, column = input of the tile; runs of 16
+    // columns go round a quarter's three warps
+    const int q4 = warp & 3;
+    const uint32_t leader_acc_empty = mapa_shared(bar_acc_empty, 0);
+    for (int n = 0; n < nunits; ++n) {
+      const Unit u = unit_at(n);
+      if (!mbar_wait_bounded(bar_acc_full, (uint32_t)n & 1u, fault, FAULT_WAIT_ACC_FULL, kWaitNs, kSleep)) break;
+      __syncwarp();
+      tcgen05_fence_after();
+      const int o = u.ot * kOTile + (int)rank * 128 + q4 * 32 + lane;
+      const int runs = pl.ni / 16, nc = two_of(u.bin) ? 2 : 1;
+      for (int r = (warp - kEpi0) >> 2; r < nc * runs; r += kNumEpi / 4) {
+        const int k = r / runs, col = (r - k * runs) * 16;
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(k * pl.ni + col), v);
+        tmem_wait_ld();
+        const int c = u.bin == 0 ? (k == 0 ? 0 : N - 1) : 2 * u.bin - 1 + k;
+        const int i = u.it * pl.ni + col;
+        if (o < args.F_out) {
+          float *dst = args.part + (((size_t)u.split * N + c) * args.F_out + o) * args.F_in + i;
+          if (args.F_in % 4 == 0) {   // whole 16-byte pieces (the partials are 256-byte aligned)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              if (i + e < args.F_in)
+                *reinterpret_cast<uint4 *>(dst + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (i + e < args.F_in) dst[e] = __uint_as_float(v[e]);
+          }
+        }
+        __syncwarp();
+      }
+      tcgen05_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(leader_acc_empty);
+    }
+  }
+
+  __syncwarp();
+  if (fault_raised(fault)) {   // give copies still in flight time to land
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
+  tcgen05_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == kProd) {
+    tcgen05_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// dW[o][i][m] = (1/N) (C_0 + (-1)^m C_{N/2} + 2 Re sum_k C_k e^{2 pi i m k / N}), C the
+// sum of the splits in order; one thread per (o, two inputs).
+template <int N, typename T>
+__global__ void __launch_bounds__(256)
+spectral_wgrad_finish_kernel(const float *__restrict__ part, int splits, int F_in, int F_out, T *__restrict__ dW,
+                             Trig trig) {
+  const int half = (F_in + 1) / 2;
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= (int64_t)F_out * half) return;
+  const int o = (int)(idx / half), i = 2 * (int)(idx % half);
+  const bool second = i + 1 < F_in;
+  const size_t plane = (size_t)F_out * F_in;
+  const float *src = part + (size_t)o * F_in + i;
+  float2 z[N], w[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) z[c] = make_float2(0.0f, 0.0f);
+  for (int s = 0; s < splits; ++s, src += N * plane)
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      z[c] = add2(z[c], make_float2(__ldg(src + c * plane), second ? __ldg(src + c * plane + 1) : 0.0f));
+  const float inv_n = 1.0f / (float)N;
+#pragma unroll
+  for (int c = 0; c < N; ++c) z[c] = scl2(z[c], c == 0 || (N % 2 == 0 && c == N - 1) ? inv_n : 2.0f * inv_n);
+  inv_dft2<N>(z, w, trig);
+  float a[N];
+#pragma unroll
+  for (int m = 0; m < N; ++m) a[m] = w[m].x;
+  store_field<N, T>(dW + ((size_t)o * F_in + i) * N, a);
+  if (second) {
+#pragma unroll
+    for (int m = 0; m < N; ++m) a[m] = w[m].y;
+    store_field<N, T>(dW + ((size_t)o * F_in + i + 1) * N, a);
+  }
+}
+
+struct DevCache {
+  int clusters[2] = {};
+};
+std::mutex g_mu;
+DevCache g_cache[64];
+
+template <bool H>
+int launch_partials(const void *Sx, const void *Sdp, float *part, int64_t T, int N, int F_in, int F_out,
+                    const Plan &plan, cudaStream_t s) {
+  auto kern = spectral_wgrad_kernel<H>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+    return set_error(EQLIN_ERR_CUDA, "cudaGetDevice failed");
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int maxc = 0;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    int &n = g_cache[dev].clusters[H];
+    if (!n) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+      if (e != cudaSuccess) return set_error(EQLIN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      cfg.gridDim = dim3(2, 1, 1);
+      cfg.dynamicSmemBytes = kSmemLimit;
+      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess || n <= 0) {
+        n = 0;
+        return set_error(EQLIN_ERR_CUDA, "cudaOccupancyMaxActiveClusters: %s", cudaGetErrorString(e));
+      }
+    }
+    maxc = n;
+  }
+  CUtensorMap md, mx;
+  int rc = tma_map_3d_16bit(&md, Sdp, (uint64_t)spectra_width(F_out), (uint64_t)T, (uint64_t)N,
+                            (uint64_t)spectra_width(F_out) * 2, 64, kTok);
+  if (rc) return rc;
+  rc = tma_map_3d_16bit(&mx, Sx, (uint64_t)spectra_width(F_in), (uint64_t)T, (uint64_t)N,
+                        (uint64_t)spectra_width(F_in) * 2, 64, kTok);
+  if (rc) return rc;
+  WgArgs a;
+  rc = fault_word_address(&a.fault);
+  if (rc) return rc;
+  a.part = part;
+  a.epoch = next_launch_epoch();
+  a.T = T;
+  a.N = N;
+  a.F_in = F_in;
+  a.F_out = F_out;
+  a.plan = plan;
+  a.units = plan.splits * plan.bins * plan.n_ot * plan.n_it;
+  a.slot_bytes = 2 * (2 + (plan.ni / 2 + 63) / 64) * kBox;
+  a.nslots = (kSmemLimit - 1024 - kCtrl) / a.slot_bytes;
+  if (a.nslots > kMaxSlots) a.nslots = kMaxSlots;
+  const int npairs = a.units < maxc ? a.units : maxc;
+  cfg.gridDim = dim3(2 * npairs, 1, 1);
+  cfg.dynamicSmemBytes = 1024 + (size_t)a.nslots * a.slot_bytes + kCtrl;
+  cfg.stream = s;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, md, mx, a);
+  if (e != cudaSuccess) return set_error(EQLIN_ERR_CUDA, "spectral weight gradient launch: %s", cudaGetErrorString(e));
+  return check_launch("spectral_wgrad_kernel");
+}
+
+template <int N, typename T>
+int launch_finish(const float *part, int splits, int F_in, int F_out, void *dW, cudaStream_t s) {
+  const int64_t n = (int64_t)F_out * ((F_in + 1) / 2);
+  spectral_wgrad_finish_kernel<N, T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(part, splits, F_in, F_out,
+                                                                                 static_cast<T *>(dW), make_trig(N));
+  return check_launch("spectral weight gradient (reduction)");
+}
+
+}  // namespace
+
+size_t gemm_tc_wgrad_bytes(int64_t T, int N, int F_in, int F_out) {
+  return (size_t)plan_for(T, N, F_in, F_out).splits * N * F_out * F_in * sizeof(float);
+}
+
+int launch_gemm_tc_wgrad(const void *Sx, const void *Sdp, void *dW, int64_t T, int N, int F_in, int F_out, int dtype,
+                         float *part, cudaStream_t s) {
+  const Plan plan = plan_for(T, N, F_in, F_out);
+  const int rc = dtype == EQLIN_F16 ? launch_partials<true>(Sx, Sdp, part, T, N, F_in, F_out, plan, s)
+                                    : launch_partials<false>(Sx, Sdp, part, T, N, F_in, F_out, plan, s);
+  if (rc) return rc;
+  switch (N) {
+#define EQLIN_CASE(NN)                                                                             \
+  case NN:                                                                                         \
+    return dtype == EQLIN_F16 ? launch_finish<NN, __half>(part, plan.splits, F_in, F_out, dW, s)   \
+                              : launch_finish<NN, __nv_bfloat16>(part, plan.splits, F_in, F_out, dW, s);
+    EQLIN_CASE(1) EQLIN_CASE(2) EQLIN_CASE(3) EQLIN_CASE(4) EQLIN_CASE(5) EQLIN_CASE(6)
+    EQLIN_CASE(7) EQLIN_CASE(8) EQLIN_CASE(9) EQLIN_CASE(10) EQLIN_CASE(11) EQLIN_CASE(12)
+    EQLIN_CASE(13) EQLIN_CASE(14) EQLIN_CASE(15) EQLIN_CASE(16)
+#undef EQLIN_CASE
+  }
+  return set_error(EQLIN_ERR_UNSUPPORTED, "N=%d not in 1..16", N);
+}
+
+}  // namespace eqlin

@@ -584,8 +584,9 @@ __device__ __forceinline__ void d8_epilogue_group(uint32_t tb, int fg, int half,
 // One 8-column group (fg) of a gated layer's epilogue for one warp (cyclic C_8;
 // output fields 2j and 2j + 1 are field j's gate and value, so the two fields
 // of a thread's item are one pair).  kEpiGated writes h = act(gate) value, 16
-// bytes per item; kEpiGates reads dh there and writes the pair's gradients
-// (dh value act'(gate), dh act(gate)), 32 contiguous bytes.  The activations
+// bytes per item; kEpiGates reads dh there, forms the pair's gradients (dh value
+// act'(gate), dh act(gate)) and writes their half spectra, which is how the data
+// and weight gradients read them: S[c][token][field], 4 bytes per coordinate.  The activations
 // are the paired forms of tc_transforms.cuh: good to well below the operand
 // rounding of the products.  Not inlined, as neg16_epilogue_group.
 template <bool H, int EPI>
@@ -627,7 +628,6 @@ __device__ __noinline__ void gated_epilogue_group(uint32_t tb, int fg, int half,
         reinterpret_cast<uint4 *>(ybase)[tok * hidden + j] = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       const uint32_t dw[4] = {dv[r8].x, dv[r8].y, dv[r8].z, dv[r8].w};
-      uint32_t wg[4], wu[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float2 g = make_float2(p[2 * q].x, p[2 * q + 1].x), u = make_float2(p[2 * q].y, p[2 * q + 1].y);
@@ -638,10 +638,16 @@ __device__ __noinline__ void gated_epilogue_group(uint32_t tb, int fg, int half,
         else if (flags & kActGelu)
           s = gelu_slope2(g, a);
         const float2 dg = mul2(mul2(d, u), s), du = mul2(d, a);
-        wg[q] = pack_x2<H>(dg.x, dg.y);
-        wu[q] = pack_x2<H>(du.x, du.y);
+        p[2 * q] = make_float2(dg.x, du.x);
+        p[2 * q + 1] = make_float2(dg.y, du.y);
       }
-      if (tok < T) st_global_v8(ybase + (tok * F_out + field_base + fg) * 16, wg, wu);
+      fwd_cyclic8(p, z);
+      const size_t plane = (size_t)T * spectra_width(F_out);
+      uint16_t *dst = reinterpret_cast<uint16_t *>(ybase) + (size_t)tok * spectra_width(F_out) + field_base + fg;
+      if (tok < T) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint32_t *>(dst + c * plane) = pack_x2<H>(z[c].x, z[c].y);
+      }
     }
   }
 }
@@ -1724,6 +1730,21 @@ int tma_map_2d_bf16(CUtensorMap *m, const void *ptr, uint64_t inner, uint64_t ou
                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, bool swizzle128) {
   return make_map_2d(m, ptr, inner, outer, row_bytes, box_inner, box_outer,
                      swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+int tma_map_3d_16bit(CUtensorMap *m, const void *ptr, uint64_t n0, uint64_t n1, uint64_t n2, uint64_t row_bytes,
+                     uint32_t box0, uint32_t box1) {
+  auto enc = get_encode_fn();
+  if (!enc) return set_error(EQLIN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[3] = {n0, n1, n2};
+  const cuuint64_t strides[2] = {row_bytes, row_bytes * n1};
+  const cuuint32_t box[3] = {box0, box1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(EQLIN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return EQLIN_OK;
 }
 
 int fault_word_address(unsigned int **out) {

@@ -235,6 +235,16 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *map, 
       : "memory");
 }
 
+// The same for a 3-D tensor map.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *map, uint32_t leader_bar,
+                                                 int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(leader_bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // L2 prefetch of one box of a 2-D tensor map (no shared memory involved).
 __device__ __forceinline__ void tma_prefetch_2d(const void *map, int32_t c0, int32_t c1) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(c0),
@@ -298,6 +308,15 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[4]
                : "r"(taddr));
 }
 
+// 32 lanes x 32 bit x 16 columns: thread t receives 16 consecutive columns of lane t.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 // 32-byte global store (dst 32-byte aligned).
 __device__ __forceinline__ void st_global_v8(void *dst, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a[0]),
@@ -338,6 +357,21 @@ __device__ __forceinline__ uint64_t smem_desc_kmajor_sw128(uint32_t addr) {
   d |= (uint64_t)2 << 61;              // layout type: 128-byte swizzle
   return d;
 }
+
+// Shared-memory matrix descriptor, MN-major, 128-byte swizzle: atoms of 64 rows
+// (M or N, 128 contiguous bytes) x 8 K-steps (1024 B), the next 64 rows `lbo`
+// bytes on, the next 8 of K 1024 B on.
+__device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;              // descriptor version for sm_100
+  d |= (uint64_t)2 << 61;              // layout type: 128-byte swizzle
+  return d;
+}
+// Instruction descriptor bits: both operands MN-major.
+constexpr uint32_t kIdescMnMajor = (1u << 15) | (1u << 16);
 
 // Instruction descriptor: kind::f16 with bf16 A/B, f32 accumulator, both
 // operands K-major, shape M x N (M = 128 for the pair instruction).

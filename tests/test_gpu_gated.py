@@ -154,7 +154,7 @@ def test_two_pass_products_every_group(N, dtype):
 
 
 def test_outputs_at_odd_addresses():
-    """h and dx 16 bytes off a 32-byte boundary: written whole, or refused when the tensor cores are asked for."""
+    """h, dx and dW 16 bytes off a 32-byte boundary are written whole."""
     T, C, H = 200, 32, 48
     x, W, dh = tensors(T, C, H, 8, BF16, 9)
     spec, adj = eq.cyclic_gated_weight_spectrum(W), eq.cyclic_gated_weight_spectrum_adjoint(W)
@@ -166,8 +166,6 @@ def test_outputs_at_odd_addresses():
     eq.cyclic_gated_backward(x, dh, spec, adj, dx=dx, dW=dW)
     near(dx, rdx, 2.5)
     near(dW, rdW, 2.5)
-    with pytest.raises(eq.EqlinError):
-        eq.cyclic_gated_backward(x, dh, spec, adj, dx=dx, path=eq.PATH_TC)
 
 
 def test_no_tokens():
