@@ -9,6 +9,7 @@ no CPU or PyTorch fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -411,6 +412,12 @@ def d8_fourier_mlp(z: torch.Tensor, W1pack: torch.Tensor, W2pack: torch.Tensor, 
 # ------------------------------------------------------------------ gated feed-forward
 
 
+# The raw handle of a device's current stream (a tenth of what a Stream object costs
+# to make, which tells in a single token's calls).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(fn, where: str, device: torch.device, *args):
     """Call an entry point with the tensors' device current, on that device's
     current stream."""
@@ -424,10 +431,6 @@ def _run(fn, where: str, device: torch.device, *args):
         raise EqlinError(rc, where)
 
 
-def _raw_stream(index: int) -> int:
-    return torch.cuda.current_stream(index).cuda_stream
-
-
 def _on(device: torch.device, t: torch.Tensor, name: str) -> int:
     """The address of t, which must be contiguous and on `device` (a GPU)."""
     if t.device != device:
@@ -439,11 +442,14 @@ def _on(device: torch.device, t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
-def _given(t: torch.Tensor | None, shape, dtype: torch.dtype, device: torch.device, name: str) -> torch.Tensor:
-    """An output of this shape: the caller's tensor, checked, or a new one."""
+def _given(t: torch.Tensor | None, shape, like: torch.Tensor, name: str, dtype: torch.dtype | None = None):
+    """An output of this shape (on like's device, of its dtype unless given): the
+    caller's tensor, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != shape or t.dtype != dtype:
+        if dtype is None and shape == like.shape and like.is_contiguous():
+            return torch.empty_like(like)
+        return like.new_empty(shape, dtype=dtype)
+    if t.shape != shape or t.dtype != (dtype or like.dtype):
         raise ValueError(f"{name} has the wrong shape or dtype")
     return t
 
@@ -457,6 +463,13 @@ def _scratch(workspace: torch.Tensor | None, need: int, device: torch.device):
     if workspace.dtype != torch.uint8:
         raise ValueError("workspace must be a byte (uint8) tensor")
     return _on(device, workspace, "workspace"), workspace.numel(), workspace
+
+
+# Buffer sizes are functions of the shape alone; a decoding loop asks for the same
+# ones at every token.
+@functools.lru_cache(maxsize=1024)
+def _bytes_of(query: str, *shape) -> int:
+    return int(getattr(_lib, query)(*shape))
 
 
 def _gated_weight(W: torch.Tensor):
@@ -479,8 +492,8 @@ def cyclic_gated_weight_spectrum(W: torch.Tensor, out: torch.Tensor | None = Non
         raise EqlinError(EQLIN_ERR_UNSUPPORTED, "eqlin_cyclic_gated_spectrum_bytes")
     if out is None:
         out = torch.empty(need, dtype=torch.uint8, device=W.device)
-    _run(_lib.eqlin_cyclic_gated_weight_spectrum, "eqlin_cyclic_gated_weight_spectrum", W.device, _on(W.device, W, "W"), N, Cin, H, dtype_code(W.dtype),
-         _on(W.device, out, "Wspec"), out.numel())
+    _run(_lib.eqlin_cyclic_gated_weight_spectrum, "eqlin_cyclic_gated_weight_spectrum", W.device,
+         _on(W.device, W, "W"), N, Cin, H, dtype_code(W.dtype), _on(W.device, out, "Wspec"), out.numel())
     return out
 
 
@@ -492,8 +505,8 @@ def cyclic_gated_weight_spectrum_adjoint(W: torch.Tensor, out: torch.Tensor | No
         raise EqlinError(EQLIN_ERR_UNSUPPORTED, "eqlin_cyclic_gated_adjoint_bytes")
     if out is None:
         out = torch.empty(need, dtype=torch.uint8, device=W.device)
-    _run(_lib.eqlin_cyclic_gated_weight_spectrum_adjoint, "eqlin_cyclic_gated_weight_spectrum_adjoint", W.device, _on(W.device, W, "W"), N, Cin, H,
-         dtype_code(W.dtype), _on(W.device, out, "Wspec_adj"), out.numel())
+    _run(_lib.eqlin_cyclic_gated_weight_spectrum_adjoint, "eqlin_cyclic_gated_weight_spectrum_adjoint", W.device,
+         _on(W.device, W, "W"), N, Cin, H, dtype_code(W.dtype), _on(W.device, out, "Wspec_adj"), out.numel())
     return out
 
 
@@ -512,20 +525,20 @@ def cyclic_gated_forward(x: torch.Tensor, Wspec: torch.Tensor, H: int, act: int 
     allocated here when not given and needed."""
     T, Cin, N = x.shape
     dt, dev = dtype_code(x.dtype), x.device
-    h = _given(h, (T, H, N), x.dtype, dev, "h")
-    spec = _spectrum_ptr(dev, Wspec, int(_lib.eqlin_cyclic_gated_spectrum_bytes(N, Cin, H, dt)), "Wspec")
-    ws, ws_bytes, _ = _scratch(workspace, int(_lib.eqlin_cyclic_gated_forward_workspace_bytes(T, N, Cin, H, dt)), dev)
-    _run(_lib.eqlin_cyclic_gated_forward, "eqlin_cyclic_gated_forward", dev, _on(dev, x, "x"), spec, _on(dev, h, "h"), T, N, Cin, H, act, dt, path,
-         ws, ws_bytes)
+    h = _given(h, (T, H, N), x, "h")
+    spec = _spectrum_ptr(dev, Wspec, _bytes_of("eqlin_cyclic_gated_spectrum_bytes", N, Cin, H, dt), "Wspec")
+    ws, ws_bytes, _ = _scratch(workspace, _bytes_of("eqlin_cyclic_gated_forward_workspace_bytes", T, N, Cin, H, dt), dev)
+    _run(_lib.eqlin_cyclic_gated_forward, "eqlin_cyclic_gated_forward", dev, _on(dev, x, "x"), spec,
+         _on(dev, h, "h"), T, N, Cin, H, act, dt, path, ws, ws_bytes)
     return h
 
 
 def cyclic_gated_forward_workspace_bytes(T: int, N: int, Cin: int, H: int, dtype: torch.dtype) -> int:
-    return int(_lib.eqlin_cyclic_gated_forward_workspace_bytes(T, N, Cin, H, dtype_code(dtype)))
+    return _bytes_of("eqlin_cyclic_gated_forward_workspace_bytes", T, N, Cin, H, dtype_code(dtype))
 
 
 def cyclic_gated_backward_workspace_bytes(T: int, N: int, Cin: int, H: int, dtype: torch.dtype) -> int:
-    return int(_lib.eqlin_cyclic_gated_backward_workspace_bytes(T, N, Cin, H, dtype_code(dtype)))
+    return _bytes_of("eqlin_cyclic_gated_backward_workspace_bytes", T, N, Cin, H, dtype_code(dtype))
 
 
 def cyclic_gated_backward(x: torch.Tensor, dh: torch.Tensor, Wspec: torch.Tensor, Wspec_adj: torch.Tensor,
@@ -539,13 +552,14 @@ def cyclic_gated_backward(x: torch.Tensor, dh: torch.Tensor, Wspec: torch.Tensor
         raise ValueError("dh has the wrong shape or dtype")
     H = dh.shape[1]
     dt, dev = dtype_code(x.dtype), x.device
-    dx = _given(dx, (T, Cin, N), x.dtype, dev, "dx")
-    dW = _given(dW, (H, 2, Cin, N), x.dtype, dev, "dW")
-    spec = _spectrum_ptr(dev, Wspec, int(_lib.eqlin_cyclic_gated_spectrum_bytes(N, Cin, H, dt)), "Wspec")
-    adj = _spectrum_ptr(dev, Wspec_adj, int(_lib.eqlin_cyclic_gated_adjoint_bytes(N, Cin, H, dt)), "Wspec_adj")
+    dx = _given(dx, (T, Cin, N), x, "dx")
+    dW = _given(dW, (H, 2, Cin, N), x, "dW")
+    spec = _spectrum_ptr(dev, Wspec, _bytes_of("eqlin_cyclic_gated_spectrum_bytes", N, Cin, H, dt), "Wspec")
+    adj = _spectrum_ptr(dev, Wspec_adj, _bytes_of("eqlin_cyclic_gated_adjoint_bytes", N, Cin, H, dt), "Wspec_adj")
     ws, ws_bytes, _ = _scratch(workspace, cyclic_gated_backward_workspace_bytes(T, N, Cin, H, x.dtype), dev)
-    _run(_lib.eqlin_cyclic_gated_backward, "eqlin_cyclic_gated_backward", dev, _on(dev, x, "x"), _on(dev, dh, "dh"), spec, adj, _on(dev, dx, "dx"),
-         _on(dev, dW, "dW"), T, N, Cin, H, act, dt, path, ws, ws_bytes)
+    _run(_lib.eqlin_cyclic_gated_backward, "eqlin_cyclic_gated_backward", dev, _on(dev, x, "x"),
+         _on(dev, dh, "dh"), spec, adj, _on(dev, dx, "dx"), _on(dev, dW, "dW"), T, N, Cin, H, act, dt, path, ws,
+         ws_bytes)
     return dx, dW
 
 
@@ -580,10 +594,10 @@ def group_norm(x: torch.Tensor, groups: int, gamma: torch.Tensor | None = None, 
     [B, groups] for group_norm_backward."""
     B, S, F, N = _norm_shape(x)
     dt, dev = dtype_code(x.dtype), x.device
-    y = _given(y, x.shape, x.dtype, dev, "y")
-    mean = _given(mean, (B, groups), torch.float32, dev, "mean")
-    rstd = _given(rstd, (B, groups), torch.float32, dev, "rstd")
-    ws, ws_bytes, _ = _scratch(workspace, int(_lib.eqlin_group_norm_workspace_bytes(B, S, F, N, groups, dt)), dev)
+    y = _given(y, x.shape, x, "y")
+    mean = _given(mean, (B, groups), x, "mean", torch.float32)
+    rstd = _given(rstd, (B, groups), mean, "rstd")
+    ws, ws_bytes, _ = _scratch(workspace, _bytes_of("eqlin_group_norm_workspace_bytes", B, S, F, N, groups, dt), dev)
     _run(_lib.eqlin_group_norm, "eqlin_group_norm", dev, _on(dev, x, "x"), _affine_ptr(gamma, F, x, "gamma"),
          _affine_ptr(beta, F, x, "beta"), _on(dev, y, "y"), _on(dev, mean, "mean"), _on(dev, rstd, "rstd"),
          B, S, F, N, groups, eps, act, dt, ws, ws_bytes)
@@ -602,13 +616,13 @@ def group_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
     for t, name in ((mean, "mean"), (rstd, "rstd")):
         if t.shape != (B, groups) or t.dtype != torch.float32:
             raise ValueError(f"{name} must be fp32 [B, groups]")
-    dx = _given(dx, x.shape, x.dtype, dev, "dx")
+    dx = _given(dx, x.shape, x, "dx")
     dgamma = torch.empty_like(gamma) if gamma is not None else None
     dbeta = torch.empty_like(beta) if beta is not None else None
     ws, ws_bytes, _ = _scratch(
-        workspace, int(_lib.eqlin_group_norm_backward_workspace_bytes(B, S, F, N, groups, dt)), dev)
-    _run(_lib.eqlin_group_norm_backward, "eqlin_group_norm_backward", dev, _on(dev, x, "x"), _on(dev, dy, "dy"), _on(dev, mean, "mean"),
-         _on(dev, rstd, "rstd"), _affine_ptr(gamma, F, x, "gamma"), _affine_ptr(beta, F, x, "beta"),
+        workspace, _bytes_of("eqlin_group_norm_backward_workspace_bytes", B, S, F, N, groups, dt), dev)
+    _run(_lib.eqlin_group_norm_backward, "eqlin_group_norm_backward", dev, _on(dev, x, "x"), _on(dev, dy, "dy"),
+         _on(dev, mean, "mean"), _on(dev, rstd, "rstd"), _affine_ptr(gamma, F, x, "gamma"), _affine_ptr(beta, F, x, "beta"),
          _on(dev, dx, "dx"), _affine_ptr(dgamma, F, x, "dgamma"), _affine_ptr(dbeta, F, x, "dbeta"),
          B, S, F, N, groups, act, dt, ws, ws_bytes)
     return dx, dgamma, dbeta

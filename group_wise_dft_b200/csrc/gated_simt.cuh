@@ -7,10 +7,10 @@
 // (rows 2j and 2j + 1 are field j's gate and value) without p reaching memory.
 //
 // Two kernels:
-//  - tiles: a CTA takes 8 kTPT tokens by 64 outputs.  A thread keeps 2 outputs
-//    x kTPT tokens x N coordinates in registers, so that one i costs 2 N weight
-//    loads (coalesced over the lanes) and kTPT N broadcast words of the shared
-//    spectrum for 2 kTPT (2N - 2) FMAs: the FMA pipe paces it, not the loads.
+//  - tiles: a CTA takes 8 TPT tokens by 64 outputs.  A thread keeps 2 outputs
+//    x TPT tokens x N coordinates in registers, so that one i costs 2 N weight
+//    loads (coalesced over the lanes) and TPT N broadcast words of the shared
+//    spectrum for 2 TPT (2N - 2) FMAs: the FMA pipe paces it, not the loads.
 //  - few tokens: with a handful of tokens the weights are what is read and
 //    only a wide split hides their latency: a CTA takes 8 outputs and splits
 //    the input fields 32 ways over its threads, joined in a fixed order.
@@ -24,12 +24,14 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <int N> struct Tile {
+// SMALL: a quarter of the tokens per CTA, for calls whose full tiles would leave
+// SMs without one (T = 2040, 256 -> 64 fields, N = 4, fp32: 32 CTAs took 139 us).
+template <int N, bool SMALL> struct Tile {
   static constexpr int NP = (N + 3) / 4 * 4;                    // coordinates per field in shared memory
-  static constexpr int TPT = N <= 4 ? 8 : 4;                    // tokens per thread
+  static constexpr int TPT = (N <= 4 ? 8 : 4) / (SMALL ? 4 : 1); // tokens per thread
   static constexpr int TT = 8 * TPT;                            // tokens per CTA
   static constexpr int IC = N <= 8 ? 16 : 8;                    // input fields per shared-memory step
-  static constexpr int CTAS = N <= 8 ? 2 : 1;                   // per SM: up to 128 or 255 registers, no spills
+  static constexpr int CTAS = N <= 8 || SMALL ? 2 : 1;          // per SM: up to 128 or 255 registers, no spills
 };
 
 template <int N>
@@ -104,11 +106,11 @@ __device__ __forceinline__ void gate_store(const DftTables &tab, const float (&G
 
 // A lane's two outputs: the pair (2j, 2j + 1) of field j, or for the plain
 // product two outputs 32 apart (any Cout, coalesced).
-template <int N, typename T, int EPI>
-__global__ void __launch_bounds__(kThreads, Tile<N>::CTAS)
+template <int N, typename T, int EPI, bool SMALL>
+__global__ void __launch_bounds__(kThreads, Tile<N, SMALL>::CTAS)
 spectral_tile_kernel(const T *__restrict__ x, const float *__restrict__ Ws, const T *__restrict__ dh,
                      T *__restrict__ out, int64_t Tn, int Cin, int Cout, int act, DftTables tab) {
-  using L = Tile<N>;
+  using L = Tile<N, SMALL>;
   __shared__ __align__(16) float Xs[L::TT][L::IC][L::NP];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t0 = (int64_t)blockIdx.x * L::TT;
@@ -300,6 +302,19 @@ spectral_few_kernel(const T *__restrict__ x, const float *__restrict__ Ws, const
 // Tokens up to which the few-token kernel runs.
 constexpr int64_t kFewTokensMost = 32;
 
+// Fewer full tiles than this (two per SM) go as small ones.
+constexpr int64_t kTileCtasLeast = 2 * 148;
+
+template <int N, typename T, int EPI, bool SMALL>
+int launch_tiles(const GatedIo &io, int act, const DftTables &tab, cudaStream_t s) {
+  constexpr int TT = Tile<N, SMALL>::TT;
+  const int64_t gx = (io.T + TT - 1) / TT, gy = ((int64_t)io.Cout + 63) / 64;
+  if (gx > 0x7fffffffLL) return set_error(EQLIN_ERR_UNSUPPORTED, "T too large for the CUDA-core grid");
+  spectral_tile_kernel<N, T, EPI, SMALL><<<dim3((unsigned)gx, (unsigned)gy), kThreads, 0, s>>>(
+      (const T *)io.x, io.Ws, (const T *)io.dh, (T *)io.out, io.T, io.Cin, io.Cout, act, tab);
+  return check_launch("gated layer");
+}
+
 template <int N, typename T, int EPI>
 int launch_ne(const GatedIo &io, int act, const DftTables &tab, cudaStream_t s) {
   if (io.T <= kFewTokensMost) {
@@ -309,13 +324,11 @@ int launch_ne(const GatedIo &io, int act, const DftTables &tab, cudaStream_t s) 
                                                                   (T *)io.out, io.T, io.Cin, io.Cout, act, tab);
     return check_launch("gated layer (few tokens)");
   }
-  const int64_t gx = (io.T + Tile<N>::TT - 1) / Tile<N>::TT;
   const int64_t gy = ((int64_t)io.Cout + 63) / 64;
-  if (gx > 0x7fffffffLL) return set_error(EQLIN_ERR_UNSUPPORTED, "T too large for the CUDA-core grid");
   if (gy > 65535) return set_error(EQLIN_ERR_UNSUPPORTED, "channel count too large for the CUDA-core grid");
-  spectral_tile_kernel<N, T, EPI><<<dim3((unsigned)gx, (unsigned)gy), kThreads, 0, s>>>(
-      (const T *)io.x, io.Ws, (const T *)io.dh, (T *)io.out, io.T, io.Cin, io.Cout, act, tab);
-  return check_launch("gated layer");
+  const int64_t full = (io.T + Tile<N, false>::TT - 1) / Tile<N, false>::TT;
+  return full * gy < kTileCtasLeast ? launch_tiles<N, T, EPI, true>(io, act, tab, s)
+                                    : launch_tiles<N, T, EPI, false>(io, act, tab, s);
 }
 
 template <int N, typename T>

@@ -581,74 +581,134 @@ __device__ __forceinline__ void d8_epilogue_group(uint32_t tb, int fg, int half,
   }
 }
 
-// One 8-column group (fg) of a gated layer's epilogue for one warp (cyclic C_8;
-// output fields 2j and 2j + 1 are field j's gate and value, so the two fields
-// of a thread's item are one pair).  kEpiGated writes h = act(gate) value, 16
-// bytes per item; kEpiGates reads dh there, forms the pair's gradients (dh value
-// act'(gate), dh act(gate)) and writes their half spectra, which is how the data
-// and weight gradients read them: S[c][token][field], 4 bytes per coordinate.  The activations
-// are the paired forms of tc_transforms.cuh: good to well below the operand
-// rounding of the products.  Not inlined, as neg16_epilogue_group.
-template <bool H, int EPI>
-__device__ __noinline__ void gated_epilogue_group(uint32_t tb, int fg, int half, int64_t tok0, int field_base,
-                                                  int64_t T, int F_out, uint8_t *ybase, const void *dh, int flags) {
+// The epilogue of 16 columns (8-column groups fg, fg + 8) of a gated layer's chunk
+// for one warp (cyclic C_8; output fields 2j and 2j + 1 are field j's gate and
+// value, so the two fields of a thread's item are one pair).  kEpiGated writes h =
+// act(gate) value, 16 bytes per item.  kEpiGates reads dh there, forms the pair's
+// gradients (dh value act'(gate), dh act(gate)) and writes their half spectra, which
+// is how the data and weight gradients read them: S[c][token][field].  A thread's
+// pair is 4 bytes of each coordinate's row; the four lanes of a quad exchange theirs
+// so that each lane has 16 bytes of two coordinates per group, 32 with the next
+// group's: whole sectors (4-byte stores took 694 us, at 160 -> 432, T = 65536).
+// The activations are the paired forms of tc_transforms.cuh: good to well below the
+// operand rounding of the products.  Not inlined, as neg16_epilogue_group.
+template <bool H>
+__device__ __forceinline__ void gated_items(uint32_t tb, int half, float2 (&p)[2][8]) {
   using namespace tc;
-  const int hidden = F_out >> 1, j = (field_base + fg) >> 1;
-  uint4 dv[2];
-  if constexpr (EPI == kEpiGates) {   // loaded first: overlaps the TMEM loads
-#pragma unroll
-    for (int r8 = 0; r8 < 2; ++r8) {
-      const int64_t tok = tok0 + 8 * r8;
-      dv[r8] = __ldcs(reinterpret_cast<const uint4 *>(dh) + (tok < T ? tok : 0) * hidden + j);
-    }
-  }
   uint32_t v[8][4];
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) tmem_ld_16x256b(tb + (uint32_t)(kk * half + fg), v[kk]);
+  for (int kk = 0; kk < 8; ++kk) tmem_ld_16x256b(tb + (uint32_t)(kk * half), v[kk]);
   tmem_wait_ld();
 #pragma unroll
   for (int r8 = 0; r8 < 2; ++r8) {   // token tok0 + 8 r8: gate in the x lanes, value in the y lanes
-    const int64_t tok = tok0 + 8 * r8;
-    float2 z[8], p[8];
+    float2 z[8];
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
       z[group_coord(kModeCyclic8, kk)] =
           make_float2(__uint_as_float(v[kk][2 * r8]), __uint_as_float(v[kk][2 * r8 + 1]));
-    inv_cyclic8(z, p);
-    if constexpr (EPI == kEpiGated) {
-      uint32_t w[4];
+    inv_cyclic8(z, p[r8]);
+  }
+}
+
+// w[0..3] of the four lanes of a quad as a 4 x 4 matrix, transposed.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int lane) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 g = make_float2(p[2 * q].x, p[2 * q + 1].x), u = make_float2(p[2 * q].y, p[2 * q + 1].y);
-        const float2 a = flags & kActSilu ? (H ? silu2(g) : silu_tanh2(g)) : (flags & kActGelu ? gelu_erf2(g) : g);
-        const float2 h = mul2(a, u);
-        w[q] = pack_x2<H>(h.x, h.y);
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t t = __shfl_xor_sync(0xffffffffu, lane & 1 ? w[i] : w[i + 1], 1);
+    if (lane & 1)
+      w[i] = t;
+    else
+      w[i + 1] = t;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t = __shfl_xor_sync(0xffffffffu, lane & 2 ? w[i] : w[i + 2], 2);
+    if (lane & 2)
+      w[i] = t;
+    else
+      w[i + 2] = t;
+  }
+}
+
+template <bool H, int EPI>
+__device__ __noinline__ void gated_epilogue_group(uint32_t tb, int fg, int half, int64_t tok0, int field_base,
+                                                  int64_t T, int F_out, uint8_t *ybase, const void *dh, int flags) {
+  using namespace tc;
+  const int hidden = F_out >> 1;
+  if constexpr (EPI == kEpiGated) {
+#pragma unroll 1
+    for (int f = fg; f < fg + 16; f += 8) {
+      float2 p[2][8];
+      gated_items<H>(tb + (uint32_t)f, half, p);
+#pragma unroll
+      for (int r8 = 0; r8 < 2; ++r8) {
+        const int64_t tok = tok0 + 8 * r8;
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 g = make_float2(p[r8][2 * q].x, p[r8][2 * q + 1].x);
+          const float2 u = make_float2(p[r8][2 * q].y, p[r8][2 * q + 1].y);
+          const float2 a = flags & kActSilu ? (H ? silu2(g) : silu_tanh2(g)) : (flags & kActGelu ? gelu_erf2(g) : g);
+          const float2 h = mul2(a, u);
+          w[q] = pack_x2<H>(h.x, h.y);
+        }
+        if (tok < T)
+          reinterpret_cast<uint4 *>(ybase)[tok * hidden + ((field_base + f) >> 1)] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if (tok < T)
-        reinterpret_cast<uint4 *>(ybase)[tok * hidden + j] = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      const uint32_t dw[4] = {dv[r8].x, dv[r8].y, dv[r8].z, dv[r8].w};
+      __syncwarp();
+    }
+  } else {
+    const int lane = threadIdx.x & 31, tq = lane & 3;
+    const int width = spectra_width(F_out);
+    uint32_t w[2][2][2][4];   // [group][token][coordinates 0..3, 4..7][lane of the quad]
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 g = make_float2(p[2 * q].x, p[2 * q + 1].x), u = make_float2(p[2 * q].y, p[2 * q + 1].y);
-        const float2 d = unpack_x2<H>(dw[q]);
-        float2 a = g, s = make_float2(1.0f, 1.0f);
-        if (flags & kActSilu)
-          s = H ? silu_slope2(g, a) : silu_slope_tanh2(g, a);
-        else if (flags & kActGelu)
-          s = gelu_slope2(g, a);
-        const float2 dg = mul2(mul2(d, u), s), du = mul2(d, a);
-        p[2 * q] = make_float2(dg.x, du.x);
-        p[2 * q + 1] = make_float2(dg.y, du.y);
+    for (int k = 0; k < 2; ++k) {
+      const int f = fg + 8 * k;
+      uint4 dv[2];
+#pragma unroll
+      for (int r8 = 0; r8 < 2; ++r8) {   // loaded first: overlaps the TMEM loads
+        const int64_t tok = tok0 + 8 * r8;
+        dv[r8] = __ldcs(reinterpret_cast<const uint4 *>(dh) + (tok < T ? tok : 0) * hidden + ((field_base + f) >> 1));
       }
-      fwd_cyclic8(p, z);
-      const size_t plane = (size_t)T * spectra_width(F_out);
-      uint16_t *dst = reinterpret_cast<uint16_t *>(ybase) + (size_t)tok * spectra_width(F_out) + field_base + fg;
-      if (tok < T) {
+      float2 p[2][8];
+      gated_items<H>(tb + (uint32_t)f, half, p);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint32_t *>(dst + c * plane) = pack_x2<H>(z[c].x, z[c].y);
+      for (int r8 = 0; r8 < 2; ++r8) {
+        const uint32_t dw[4] = {dv[r8].x, dv[r8].y, dv[r8].z, dv[r8].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 g = make_float2(p[r8][2 * q].x, p[r8][2 * q + 1].x);
+          const float2 u = make_float2(p[r8][2 * q].y, p[r8][2 * q + 1].y);
+          const float2 d = unpack_x2<H>(dw[q]);
+          float2 a = g, s = make_float2(1.0f, 1.0f);
+          if (flags & kActSilu)
+            s = H ? silu_slope2(g, a) : silu_slope_tanh2(g, a);
+          else if (flags & kActGelu)
+            s = gelu_slope2(g, a);
+          const float2 dg = mul2(mul2(d, u), s), du = mul2(d, a);
+          p[r8][2 * q] = make_float2(dg.x, du.x);
+          p[r8][2 * q + 1] = make_float2(dg.y, du.y);
+        }
+        float2 z[8];
+        fwd_cyclic8(p[r8], z);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[k][r8][c >> 2][c & 3] = pack_x2<H>(z[c].x, z[c].y);
+        quad_transpose(w[k][r8][0], lane);
+        quad_transpose(w[k][r8][1], lane);
       }
     }
+    // lane tq of a quad now has coordinates tq and 4 + tq of the quad's 16 fields
+    const int field0 = field_base - 2 * tq + fg;
+#pragma unroll
+    for (int r8 = 0; r8 < 2; ++r8) {
+      const int64_t tok = tok0 + 8 * r8;
+      if (tok < T) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          st_global_v8(ybase + (((size_t)(4 * b + tq) * T + tok) * width + field0) * 2, w[0][r8][b], w[1][r8][b]);
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -1058,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t tok0 = (int64_t)(pair + ti * npairs) * kTileTokens + (int64_t)rank * kRowsPerCta +
                              (q4 & 1) * 32 + sub * 16 + tr;
         const int field_base = c * kCoMax + h * half + 2 * tq;
-        for (int fg = 8; fg < half; fg += 16) {
+        for (int fg = kGated ? 16 : 8; fg < half; fg += kGated ? 32 : 16) {
           if constexpr (kGated)
             gated_epilogue_group<H, EPI>(tb, fg, half, tok0, field_base, args.T, F_out, ybase, args.y_even,
                                          args.gelu);
@@ -1176,7 +1236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int field_base = c * kCoMax + h * half + 2 * tq;
       // D8: the epilogue warps take the even 8-column groups, transform warps
       // 0..7 the odd ones (kD8HelpWarps)
-      for (int fg = 0; fg < half; fg += (transform_warps_help_epilogue<MODE, kGated>() ? 16 : 8)) {
+      // (the gated epilogues go by two groups at a time)
+      for (int fg = 0; fg < half; fg += (kGated ? 32 : transform_warps_help_epilogue<MODE>() ? 16 : 8)) {
         if constexpr (MODE == kModeD8) {
           d8_epilogue_group<H>(tb, fg, half, tok0, field_base, T, F_out, ybase, args.gelu);
           continue;
