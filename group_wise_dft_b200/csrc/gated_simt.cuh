@@ -8,9 +8,10 @@
 //
 // Two kernels:
 //  - tiles: a CTA takes 8 TPT tokens by 64 outputs.  A thread keeps 2 outputs
-//    x TPT tokens x N coordinates in registers, so that one i costs 2 N weight
-//    loads (coalesced over the lanes) and TPT N broadcast words of the shared
-//    spectrum for 2 TPT (2N - 2) FMAs: the FMA pipe paces it, not the loads.
+//    x TPT tokens x N coordinates in registers, so that one input field costs N
+//    8-byte weight words and TPT N broadcast spectrum words from shared memory for
+//    2 TPT (2N - 2) FMAs.  The next step's weights (cp.async) and x are on their
+//    way while a step is computed.
 //  - few tokens: with a handful of tokens the weights are what is read and
 //    only a wide split hides their latency: a CTA takes 8 outputs and splits
 //    the input fields 32 ways over its threads, joined in a fixed order.
@@ -23,6 +24,7 @@ namespace eqlin {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kOut = 64;         // outputs per CTA of the tile kernel
 
 // SMALL: a quarter of the tokens per CTA, for calls whose full tiles would leave
 // SMs without one (T = 2040, 256 -> 64 fields, N = 4, fp32: 32 CTAs took 139 us).
@@ -30,7 +32,7 @@ template <int N, bool SMALL> struct Tile {
   static constexpr int NP = (N + 3) / 4 * 4;                    // coordinates per field in shared memory
   static constexpr int TPT = (N <= 4 ? 8 : 4) / (SMALL ? 4 : 1); // tokens per thread
   static constexpr int TT = 8 * TPT;                            // tokens per CTA
-  static constexpr int IC = N <= 8 ? 16 : 8;                    // input fields per shared-memory step
+  static constexpr int IC = 8;                                  // input fields per shared-memory step
   static constexpr int CTAS = N <= 8 || SMALL ? 2 : 1;          // per SM: up to 128 or 255 registers, no spills
 };
 
@@ -104,20 +106,40 @@ __device__ __forceinline__ void gate_store(const DftTables &tab, const float (&G
   }
 }
 
-// A lane's two outputs: the pair (2j, 2j + 1) of field j, or for the plain
-// product two outputs 32 apart (any Cout, coalesced).
+__device__ __forceinline__ void cp_async(void *smem, const void *src, int bytes, bool valid) {
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(smem);
+  const int n = valid ? bytes : 0;   // nothing is read then, and zeros are written
+  if (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else if (bytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// Shared memory of a tile CTA, in floats: two buffers of weights [IC][N][64] and of
+// spectra [TT][IC][NP].
+template <int N, bool SMALL>
+constexpr int tile_smem_floats() {
+  using L = Tile<N, SMALL>;
+  return 2 * (L::IC * N * kOut + L::TT * L::IC * L::NP);
+}
+
+// A lane's two outputs are 2 lane and 2 lane + 1 of the CTA's 64: field j's gate and
+// value where the epilogue gates.  W: weights per cp.async (4, 2 or 1 floats, by
+// Cout's divisors).
 template <int N, typename T, int EPI, bool SMALL>
 __global__ void __launch_bounds__(kThreads, Tile<N, SMALL>::CTAS)
 spectral_tile_kernel(const T *__restrict__ x, const float *__restrict__ Ws, const T *__restrict__ dh,
-                     T *__restrict__ out, int64_t Tn, int Cin, int Cout, int act, DftTables tab) {
+                     T *__restrict__ out, int64_t Tn, int Cin, int Cout, int act, int wide, DftTables tab) {
   using L = Tile<N, SMALL>;
-  __shared__ __align__(16) float Xs[L::TT][L::IC][L::NP];
+  extern __shared__ __align__(16) float tile_smem[];
+  constexpr int kW = L::IC * N * kOut, kX = L::TT * L::IC * L::NP;
+  constexpr int kItems = (L::TT * L::IC + kThreads - 1) / kThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t0 = (int64_t)blockIdx.x * L::TT;
-  const int o0 = blockIdx.y * 64;
-  const int oa = EPI == kEpiLinear ? o0 + lane : o0 + 2 * lane;
-  const int ob = EPI == kEpiLinear ? oa + 32 : oa + 1;
-  const bool has_a = oa < Cout, has_b = ob < Cout;
+  const int o0 = blockIdx.y * kOut;
+  const int oa = o0 + 2 * lane;
 
   float acc[2][L::TPT][N];
 #pragma unroll
@@ -127,44 +149,71 @@ spectral_tile_kernel(const T *__restrict__ x, const float *__restrict__ Ws, cons
 #pragma unroll
       for (int c = 0; c < N; ++c) acc[p][a][c] = 0.f;
 
-  for (int i0 = 0; i0 < Cin; i0 += L::IC) {
-    __syncthreads();
-    for (int p = threadIdx.x; p < L::TT * L::IC; p += kThreads) {
-      const int tl = p / L::IC, il = p % L::IC;
+  // weights of the fields i0 .. i0 + IC into buffer b (asynchronous)
+  auto load_w = [&](int i0, int b) {
+    float *dst = tile_smem + b * kW;
+    const int per_row = kOut / wide, rows = min(L::IC, Cin - i0) * N;
+    for (int p = threadIdx.x; p < rows * per_row; p += kThreads) {
+      const int row = p / per_row, q = (p - row * per_row) * wide;
+      const bool valid = o0 + q < Cout;   // `wide` divides Cout: whole or not at all
+      cp_async(dst + row * kOut + q, Ws + ((size_t)i0 * N + row) * Cout + (valid ? o0 + q : 0), 4 * wide, valid);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // x of those fields into registers, and their spectra into buffer b
+  float v[kItems][N];
+  auto load_x = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int p = threadIdx.x + k * kThreads, tl = p / L::IC, i = i0 + p % L::IC;
       const int64_t t = t0 + tl;
-      const int i = i0 + il;
-      float v[N], X[N];
-      if (t < Tn && i < Cin) {
-        load_field<N, T>(x + ((size_t)t * Cin + i) * N, v);
+      if (p < L::TT * L::IC && t < Tn && i < Cin) {
+        load_field<N, T>(x + ((size_t)t * Cin + i) * N, v[k]);
       } else {
 #pragma unroll
-        for (int h = 0; h < N; ++h) v[h] = 0.f;
+        for (int h = 0; h < N; ++h) v[k][h] = 0.f;
       }
-      forward_dft<N>(tab, v, X);
-#pragma unroll
-      for (int c = 0; c < N; ++c) Xs[tl][il][c] = X[c];
     }
-    __syncthreads();
+  };
+  auto store_x = [&](int b) {
+    float *dst = tile_smem + 2 * kW + b * kX;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int p = threadIdx.x + k * kThreads;
+      if (p >= L::TT * L::IC) continue;
+      float X[N];
+      forward_dft<N>(tab, v[k], X);
+#pragma unroll
+      for (int c = 0; c < N; ++c) dst[p * L::NP + c] = X[c];
+    }
+  };
+
+  load_w(0, 0);
+  load_x(0);
+  store_x(0);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  int b = 0;
+  for (int i0 = 0; i0 < Cin; i0 += L::IC, b ^= 1) {
+    const bool more = i0 + L::IC < Cin;
+    if (more) {   // the next step's operands, on their way while this one is computed
+      load_w(i0 + L::IC, b ^ 1);
+      load_x(i0 + L::IC);
+    }
+    const float *Wb = tile_smem + b * kW + 2 * lane, *Xb = tile_smem + 2 * kW + b * kX;
     const int iend = min(L::IC, Cin - i0);
 #pragma unroll 2
     for (int il = 0; il < iend; ++il) {
       float wa[N], wb[N];
-      const float *wp = Ws + (size_t)(i0 + il) * N * Cout;
 #pragma unroll
       for (int c = 0; c < N; ++c) {
-        if constexpr (EPI == kEpiLinear) {
-          wa[c] = has_a ? __ldg(wp + (size_t)c * Cout + oa) : 0.f;
-          wb[c] = has_b ? __ldg(wp + (size_t)c * Cout + ob) : 0.f;
-        } else {   // Cout is even: the pair is one aligned 8-byte word
-          const float2 w = has_a ? __ldg(reinterpret_cast<const float2 *>(wp + (size_t)c * Cout + oa))
-                                 : make_float2(0.f, 0.f);
-          wa[c] = w.x;
-          wb[c] = w.y;
-        }
+        const float2 w = *reinterpret_cast<const float2 *>(Wb + (il * N + c) * kOut);
+        wa[c] = w.x;
+        wb[c] = w.y;
       }
 #pragma unroll
       for (int a = 0; a < L::TPT; ++a) {
-        const float4 *src = reinterpret_cast<const float4 *>(Xs[warp * L::TPT + a][il]);
+        const float4 *src = reinterpret_cast<const float4 *>(Xb + ((warp * L::TPT + a) * L::IC + il) * L::NP);
         float X[N];
 #pragma unroll
         for (int c = 0; c < N; c += 4) {
@@ -178,8 +227,11 @@ spectral_tile_kernel(const T *__restrict__ x, const float *__restrict__ Ws, cons
         bin_products<N>(acc[1][a], wb, X);
       }
     }
+    if (more) store_x(b ^ 1);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
   }
-  if (!has_a) return;
+  if (oa >= Cout) return;
 #pragma unroll
   for (int a = 0; a < L::TPT; ++a) {
     const int64_t t = t0 + warp * L::TPT + a;
@@ -188,9 +240,9 @@ spectral_tile_kernel(const T *__restrict__ x, const float *__restrict__ Ws, cons
       float y[N];
       inverse_dft<N>(tab, acc[0][a], y);
       store_field<N, T>(out + ((size_t)t * Cout + oa) * N, y);
-      if (has_b) {
+      if (oa + 1 < Cout) {
         inverse_dft<N>(tab, acc[1][a], y);
-        store_field<N, T>(out + ((size_t)t * Cout + ob) * N, y);
+        store_field<N, T>(out + ((size_t)t * Cout + oa + 1) * N, y);
       }
     } else {
       gate_store<N, T, EPI>(tab, acc[0][a], acc[1][a], dh, out, t, oa >> 1, Cout >> 1, act);
@@ -302,16 +354,23 @@ spectral_few_kernel(const T *__restrict__ x, const float *__restrict__ Ws, const
 // Tokens up to which the few-token kernel runs.
 constexpr int64_t kFewTokensMost = 32;
 
-// Fewer full tiles than this (two per SM) go as small ones.
-constexpr int64_t kTileCtasLeast = 2 * 148;
+// Fewer full tiles than half the SMs go as small ones.
+constexpr int64_t kTileCtasLeast = 74;
 
 template <int N, typename T, int EPI, bool SMALL>
 int launch_tiles(const GatedIo &io, int act, const DftTables &tab, cudaStream_t s) {
   constexpr int TT = Tile<N, SMALL>::TT;
   const int64_t gx = (io.T + TT - 1) / TT, gy = ((int64_t)io.Cout + 63) / 64;
   if (gx > 0x7fffffffLL) return set_error(EQLIN_ERR_UNSUPPORTED, "T too large for the CUDA-core grid");
-  spectral_tile_kernel<N, T, EPI, SMALL><<<dim3((unsigned)gx, (unsigned)gy), kThreads, 0, s>>>(
-      (const T *)io.x, io.Ws, (const T *)io.dh, (T *)io.out, io.T, io.Cin, io.Cout, act, tab);
+  constexpr int smem = tile_smem_floats<N, SMALL>() * (int)sizeof(float);
+  auto kern = spectral_tile_kernel<N, T, EPI, SMALL>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return set_error(EQLIN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  }
+  const int wide = io.Cout % 4 == 0 ? 4 : io.Cout % 2 == 0 ? 2 : 1;
+  kern<<<dim3((unsigned)gx, (unsigned)gy), kThreads, smem, s>>>((const T *)io.x, io.Ws, (const T *)io.dh, (T *)io.out,
+                                                                io.T, io.Cin, io.Cout, act, wide, tab);
   return check_launch("gated layer");
 }
 
