@@ -91,6 +91,11 @@ _SIGS = {
     "eqlin_group_norm_backward_workspace_bytes": (_sz, [_i64, _i64, _i, _i, _i, _i]),
     "eqlin_group_norm_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i, _i, _i, _i,
                                        _i, _vp, _sz, _vp]),
+    "eqlin_cyclic_gated_mlp_contract_bytes": (_sz, [_i, _i, _i, _i]),
+    "eqlin_cyclic_gated_mlp_contract_spectrum": (_i, [_vp, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "eqlin_cyclic_gated_mlp_workspace_bytes": (_sz, [_i64, _i, _i, _i, _i, _i]),
+    "eqlin_cyclic_gated_mlp": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _i, ctypes.c_float, _i, _i, _i,
+                                    _vp, _sz, _vp]),
     "eqlin_selftest_wait_timeout": (_i, [ctypes.c_uint64, _i, _vp, _vp]),
 }
 
@@ -626,6 +631,46 @@ def group_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
          _on(dev, dx, "dx"), _affine_ptr(dgamma, F, x, "dgamma"), _affine_ptr(dbeta, F, x, "dbeta"),
          B, S, F, N, groups, act, dt, ws, ws_bytes)
     return dx, dgamma, dbeta
+
+
+# ------------------------------------------------------------------ feed-forward block
+
+
+def cyclic_gated_mlp_contract_spectrum(W: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """W [Cin, H, N] (device) -> opaque spectrum of the block's contraction H -> Cin."""
+    Cin, H, N = W.shape
+    need = int(_lib.eqlin_cyclic_gated_mlp_contract_bytes(N, H, Cin, dtype_code(W.dtype)))
+    if need == 0:
+        raise EqlinError(EQLIN_ERR_UNSUPPORTED, "eqlin_cyclic_gated_mlp_contract_bytes")
+    if out is None:
+        out = torch.empty(need, dtype=torch.uint8, device=W.device)
+    _run(_lib.eqlin_cyclic_gated_mlp_contract_spectrum, "eqlin_cyclic_gated_mlp_contract_spectrum", W.device,
+         _on(W.device, W, "W"), N, H, Cin, dtype_code(W.dtype), _on(W.device, out, "Wspec"), out.numel())
+    return out
+
+
+def cyclic_gated_mlp_workspace_bytes(T: int, N: int, Cin: int, H: int, groups: int, dtype: torch.dtype) -> int:
+    return _bytes_of("eqlin_cyclic_gated_mlp_workspace_bytes", T, N, Cin, H, groups, dtype_code(dtype))
+
+
+def cyclic_gated_mlp(x: torch.Tensor, W1spec: torch.Tensor, W2spec: torch.Tensor, H: int, groups: int = 0,
+                     gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None, eps: float = 1e-5,
+                     act: int = ACT_SILU, y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     path: int = PATH_AUTO) -> torch.Tensor:
+    """The feed-forward block x [T, Cin, N] (device) -> y [T, Cin, N]: token group
+    norm (groups = 0: none), gated layer to H fields (cyclic_gated_weight_spectrum),
+    contraction (cyclic_gated_mlp_contract_spectrum).  The workspace (a device byte
+    tensor of cyclic_gated_mlp_workspace_bytes) is allocated here when not given."""
+    T, Cin, N = x.shape
+    dt, dev = dtype_code(x.dtype), x.device
+    y = _given(y, x.shape, x, "y")
+    w1 = _spectrum_ptr(dev, W1spec, _bytes_of("eqlin_cyclic_gated_spectrum_bytes", N, Cin, H, dt), "W1spec")
+    w2 = _spectrum_ptr(dev, W2spec, _bytes_of("eqlin_cyclic_gated_mlp_contract_bytes", N, H, Cin, dt), "W2spec")
+    ws, ws_bytes, _ = _scratch(workspace, cyclic_gated_mlp_workspace_bytes(T, N, Cin, H, groups, x.dtype), dev)
+    _run(_lib.eqlin_cyclic_gated_mlp, "eqlin_cyclic_gated_mlp", dev, _on(dev, x, "x"),
+         _affine_ptr(gamma, Cin, x, "gamma"), _affine_ptr(beta, Cin, x, "beta"), w1, w2, _on(dev, y, "y"), T, N, Cin, H,
+         groups, eps, act, dt, path, ws, ws_bytes)
+    return y
 
 
 # ------------------------------------------------------------------ host-resident data

@@ -53,6 +53,9 @@ SpecLayout spec_layout(int N, int Cin, int H, int dtype) {
   const Tc k = tc_kind(N, Cin, H, dtype);
   return layout(N, Cin, 2 * H, k == kTcFused ? cyclic_tc_bytes(N, Cin, 2 * H) : k == kTcGemm ? gemm_tc_bytes(N, Cin, 2 * H) : 0);
 }
+SpecLayout contract_layout(int N, int H, int Cout, int dtype) {
+  return layout(N, H, Cout, gemm_tc_supported(N, H, Cout, dtype) ? gemm_tc_bytes(N, H, Cout) : 0);
+}
 SpecLayout adjoint_layout(int N, int Cin, int H, int dtype) {
   return layout(N, 2 * H, Cin, tc_kind(N, Cin, H, dtype) != kTcNone ? gemm_tc_bytes(N, 2 * H, Cin) : 0);
 }
@@ -116,6 +119,28 @@ int weight_spectrum(const void *W, int N, int Cin, int H, int dtype, bool adjoin
   CyclicSpecLayout C{};   // the fp32 section alone
   return adjoint ? launch_cyclic_spectrum(W, N, 2 * H, Cin, dtype, 1, out, C, s)
                  : launch_cyclic_spectrum(W, N, Cin, 2 * H, dtype, 0, out, C, s);
+}
+
+// The block's workspace: the normalised x, the hidden layer, then what the gated
+// layer, the norm or the contraction needs (one at a time).
+struct MlpParts {
+  size_t hidden, scratch, total;   // (the normalised x at 0)
+};
+MlpParts mlp_parts(int64_t T, int N, int Cin, int H, int G, int dtype) {
+  MlpParts p{};
+  p.hidden = G > 0 ? round256((size_t)T * Cin * N * elem_size(dtype)) : 0;
+  p.scratch = p.hidden + round256((size_t)T * H * N * elem_size(dtype));
+  size_t most = forward_workspace(T, N, Cin, H, dtype);
+  if (G > 0) {
+    const size_t norm = round256(eqlin_group_norm_workspace_bytes(T, 1, Cin, N, G, dtype));
+    if (norm > most) most = norm;
+  }
+  if (gemm_tc_supported(N, H, Cin, dtype)) {
+    const size_t spectra = round256(gemm_tc_spectra_bytes(T, N, H));
+    if (spectra > most) most = spectra;
+  }
+  p.total = p.scratch + most;
+  return p;
 }
 
 }  // namespace
@@ -267,6 +292,83 @@ int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec
   if (!dW) return EQLIN_OK;
   return eqlin_cyclic_weight_grad_ex(x, ws, dW, T, N, Cin, 2 * H, dtype, ws + p.part, workspace_bytes - p.part,
                                      EQLIN_PATH_SIMT, stream);
+}
+
+size_t eqlin_cyclic_gated_mlp_contract_bytes(int N, int H, int Cin, int dtype) {
+  if (check_shape(N, Cin, H, dtype) != EQLIN_OK) return 0;
+  return contract_layout(N, H, Cin, dtype).total;
+}
+
+int eqlin_cyclic_gated_mlp_contract_spectrum(const void *W, int N, int H, int Cin, int dtype, void *Wspec,
+                                             size_t Wspec_bytes, eqlin_stream_t stream) {
+  clear_error();
+  int rc = check_shape(N, Cin, H, dtype);
+  if (rc) return rc;
+  if (!W || !Wspec) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(W, 16) || !aligned(Wspec, 16))
+    return set_error(EQLIN_ERR_ALIGN, "W and the spectrum must be 16-byte aligned");
+  const SpecLayout L = contract_layout(N, H, Cin, dtype);
+  if (Wspec_bytes < L.total)
+    return set_error(EQLIN_ERR_SIZE, "spectrum buffer of %zu bytes < required %zu", Wspec_bytes, L.total);
+  if (L.tc_bytes)
+    return launch_gemm_tc_pack(W, N, H, Cin, false, dtype, Wspec, static_cast<char *>(Wspec) + L.tc_offset,
+                               (cudaStream_t)stream);
+  CyclicSpecLayout C{};   // the fp32 section alone
+  return launch_cyclic_spectrum(W, N, H, Cin, dtype, 0, Wspec, C, (cudaStream_t)stream);
+}
+
+size_t eqlin_cyclic_gated_mlp_workspace_bytes(int64_t T, int N, int Cin, int H, int G, int dtype) {
+  if (check_shape(N, Cin, H, dtype) != EQLIN_OK || T <= 0 || G < 0 || (G > 0 && Cin % G != 0) ||
+      check_call(T, N, Cin, H, EQLIN_ACT_NONE, EQLIN_PATH_AUTO) != EQLIN_OK)
+    return 0;
+  return mlp_parts(T, N, Cin, H, G, dtype).total;
+}
+
+int eqlin_cyclic_gated_mlp(const void *x, const void *gamma, const void *beta, const void *W1spec, const void *W2spec,
+                           void *y, int64_t T, int N, int Cin, int H, int G, float eps, int act, int dtype, int path,
+                           void *workspace, size_t workspace_bytes, eqlin_stream_t stream) {
+  clear_error();
+  int rc = check_shape(N, Cin, H, dtype);
+  if (rc || (rc = check_call(T, N, Cin, H, act, path))) return rc;
+  if (G < 0 || (G > 0 && Cin % G != 0))
+    return set_error(EQLIN_ERR_INVALID_ARG, "Cin=%d must be a multiple of G=%d groups (0: no norm)", Cin, G);
+  Tc k = tc_for(T, N, Cin, H, dtype, path);
+  if (path == EQLIN_PATH_TC && (k == kTcNone || !gemm_tc_supported(N, H, Cin, dtype)))
+    return set_error(EQLIN_ERR_UNSUPPORTED, "%s", kTcNeeds);
+  if (T == 0) return EQLIN_OK;
+  if (!x || !W1spec || !W2spec || !y) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(W1spec, 16) || !aligned(W2spec, 16))
+    return set_error(EQLIN_ERR_ALIGN, "x, y and the spectra must be 16-byte aligned");
+  const MlpParts p = mlp_parts(T, N, Cin, H, G, dtype);
+  if (!workspace) return set_error(EQLIN_ERR_INVALID_ARG, "null workspace");
+  if (workspace_bytes < p.total)
+    return set_error(EQLIN_ERR_SIZE, "workspace_bytes=%zu < required %zu", workspace_bytes, p.total);
+  if (!aligned(workspace, 256)) return set_error(EQLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
+  char *ws = static_cast<char *>(workspace);
+  void *hidden = ws + p.hidden, *scratch = ws + p.scratch;
+  const size_t scratch_bytes = workspace_bytes - p.scratch;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (G > 0) {
+    rc = eqlin_group_norm(x, gamma, beta, ws, nullptr, nullptr, T, 1, Cin, N, G, eps, EQLIN_ACT_NONE, dtype, scratch,
+                          scratch_bytes, stream);
+    if (rc) return rc;
+    x = ws;
+  }
+  rc = eqlin_cyclic_gated_forward(x, W1spec, hidden, T, N, Cin, H, act, dtype, path, scratch, scratch_bytes, stream);
+  if (rc) return rc;
+  if (k != kTcNone && gemm_tc_supported(N, H, Cin, dtype)) {
+    if ((rc = launch_gemm_tc_spectra(hidden, scratch, T, N, H, dtype, s))) return rc;
+    return launch_gemm_tc(kEpiLinear, scratch, tc_section(W2spec, contract_layout(N, H, Cin, dtype)), nullptr, y, T, N,
+                          H, Cin, EQLIN_ACT_NONE, dtype, s);
+  }
+  GatedIo io{};
+  io.x = hidden;
+  io.Ws = fp32_section(W2spec);
+  io.out = y;
+  io.T = T;
+  io.Cin = H;
+  io.Cout = Cin;
+  return launch_gated_simt(kEpiLinear, io, N, EQLIN_ACT_NONE, dtype, s);
 }
 
 }  // extern "C"

@@ -437,6 +437,27 @@ EQLIN_API int eqlin_group_norm_backward(const void *x, const void *dy, const flo
                               int64_t B, int64_t S, int F, int N, int G, int act, int dtype,
                               void *workspace, size_t workspace_bytes, eqlin_stream_t stream);
 
+/* ------------------------------------------------------ the whole block */
+
+/* The feed-forward block of a pre-norm transformer over C_N, forward:
+ *     y = contract(gated(norm(x))),
+ * norm the token group norm above (S = 1, G groups, no activation; G = 0: none),
+ * gated the gated layer Cin -> H (W1spec from eqlin_cyclic_gated_weight_spectrum),
+ * contract the cyclic layer H -> Cin of W2, device [Cin][H][N], any H (W2spec from
+ * eqlin_cyclic_gated_mlp_contract_spectrum, of at least ..._contract_bytes).  x, y:
+ * device [T][Cin][N]; gamma, beta as in eqlin_group_norm.  The residual is the
+ * caller's to add.  The intermediate values are rounded to `dtype`; they live in
+ * the workspace (256-byte aligned, at least ..._workspace_bytes).  Paths as in
+ * eqlin_cyclic_gated_forward. */
+EQLIN_API size_t eqlin_cyclic_gated_mlp_contract_bytes(int N, int H, int Cin, int dtype);
+EQLIN_API int eqlin_cyclic_gated_mlp_contract_spectrum(const void *W, int N, int H, int Cin, int dtype, void *Wspec,
+                                             size_t Wspec_bytes, eqlin_stream_t stream);
+EQLIN_API size_t eqlin_cyclic_gated_mlp_workspace_bytes(int64_t T, int N, int Cin, int H, int G, int dtype);
+EQLIN_API int eqlin_cyclic_gated_mlp(const void *x, const void *gamma, const void *beta, const void *W1spec,
+                           const void *W2spec, void *y, int64_t T, int N, int Cin, int H, int G, float eps,
+                           int act, int dtype, int path, void *workspace, size_t workspace_bytes,
+                           eqlin_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
