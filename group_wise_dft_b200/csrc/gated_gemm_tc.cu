@@ -55,18 +55,30 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kSleep = 64;
 
-// Most output fields per group: all coordinates of a unit in TMEM.
-__host__ __device__ inline int co_most(int N) {
-  const int co = 2 * (int)kTmemCols / N / kCoStep * kCoStep;
+// Stages of 64 input fields: the real bins 0 and N / 2, then the complex bins.
+__host__ __device__ inline int num_complex(int N) { return (N - 1) / 2; }
+__host__ __device__ inline bool has_mid(int N) { return N > 1 && N % 2 == 0; }
+__host__ __device__ inline int num_stages(int N) { return 1 + num_complex(N); }
+__host__ __device__ inline int k_blocks(int F_in) { return (F_in + kK - 1) / kK; }
+
+// Most output fields per group.  All coordinates of a unit lie in TMEM; with half
+// of it per unit the epilogue of one runs under the next one's products, with all
+// of it a stage's A serves twice the outputs.  Long products (kLongStages stages or
+// more) take the latter.
+constexpr int kLongStages = 32;
+__host__ __device__ inline int co_most(int N, int F_in) {
+  const bool all = k_blocks(F_in) * num_stages(N) >= kLongStages;
+  const int co = (all ? 2 : 1) * (int)kTmemCols / N / kCoStep * kCoStep;
   return co < 128 ? co : 128;
 }
 // Output fields in 32-field blocks (the last may be padding in part: zero
 // weights, no stores), dealt out evenly to the groups.
 struct Groups {
   int blocks, n;
-  __host__ __device__ Groups(int F_out, int N) {
+  __host__ __device__ Groups(int F_in, int F_out, int N) {
+    const int most = co_most(N, F_in);
     blocks = (F_out + kCoStep - 1) / kCoStep;
-    n = (blocks * kCoStep + co_most(N) - 1) / co_most(N);
+    n = (blocks * kCoStep + most - 1) / most;
   }
   __host__ __device__ int co(int g) const { return kCoStep * (blocks / n + (g < blocks % n ? 1 : 0)); }
   __host__ __device__ int first(int g) const {
@@ -74,11 +86,6 @@ struct Groups {
     return kCoStep * (g * (blocks / n) + (g < r ? g : r));
   }
 };
-// Stages of 64 input fields: the real bins 0 and N / 2, then the complex bins.
-__host__ __device__ inline int num_complex(int N) { return (N - 1) / 2; }
-__host__ __device__ inline bool has_mid(int N) { return N > 1 && N % 2 == 0; }
-__host__ __device__ inline int num_stages(int N) { return 1 + num_complex(N); }
-__host__ __device__ inline int k_blocks(int F_in) { return (F_in + kK - 1) / kK; }
 // First 128-byte row of the packed weights of (group, 64 input fields kb, stage,
 // CTA half); a half is co rows: W_0 of its co / 2 fields, then W_{N/2} (stage 0),
 // or Wi, then Wr.
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(256)
 pack_gemm_kernel(const T *__restrict__ W, int F_in, int F_out, float *__restrict__ Ws, uint32_t *__restrict__ dst,
                  Trig trig) {
   __shared__ float sm[kK * N][9];
-  const Groups gr(F_out, N);
+  const Groups gr(F_in, F_out, N);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int kb = blockIdx.x, o0 = blockIdx.y * 8, o = o0 + warp, i = kb * kK + 2 * lane;
   float a[N], b[N];
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const FaultCtx fault{args.fault, args.epoch};
   const int N = args.N, F_in = args.F_in;
-  const Groups gr(args.F_out, N);
+  const Groups gr(args.F_in, args.F_out, N);
   const int nkb = k_blocks(F_in), nst = num_stages(N);
   const uint32_t bufs = (uint32_t)args.bufs;
 
@@ -514,7 +521,7 @@ int launch_gemm(const void *S, const void *pack, const void *dh, void *out, int6
     }
     maxc = n;
   }
-  const Groups gr(F_out, N);
+  const Groups gr(F_in, F_out, N);
   const int co_big = gr.co(0), co_small = gr.co(gr.n - 1);
   CUtensorMap ms, mb, mt;
   int rc = tma_map_2d_bf16(&ms, S, (uint64_t)spectra_width(F_in), (uint64_t)T * N, (uint64_t)spectra_width(F_in) * 2, kK, kRows, true);
@@ -562,7 +569,7 @@ int launch_spectra(const void *x, void *S, int64_t Tn, int F, cudaStream_t s) {
 
 template <int N, typename T, bool H>
 int launch_pack(const void *W, int F_in, int F_out, bool adjoint, void *Ws, void *dst, cudaStream_t s) {
-  const dim3 grid((unsigned)k_blocks(F_in), (unsigned)(Groups(F_out, N).blocks * kCoStep / 8));
+  const dim3 grid((unsigned)k_blocks(F_in), (unsigned)(Groups(F_in, F_out, N).blocks * kCoStep / 8));
   if (grid.y > 65535) return set_error(EQLIN_ERR_UNSUPPORTED, "channel count too large");
   const T *w = static_cast<const T *>(W);
   if (adjoint)
@@ -582,14 +589,15 @@ bool gemm_tc_supported(int N, int F_in, int F_out, int dtype) {
 }
 
 size_t gemm_tc_bytes(int N, int F_in, int F_out) {
-  const Groups gr(F_out, N);
+  const Groups gr(F_in, F_out, N);
   return (size_t)weight_row(gr, F_in, N, gr.n - 1, k_blocks(F_in), 0, 0) * 128;
 }
 
 size_t gemm_tc_spectra_bytes(int64_t T, int N, int F) { return (size_t)T * N * spectra_width(F) * 2; }
 
 bool gemm_tc_tokens_ok(int64_t T, int N, int F_out) {
-  return T <= (int64_t)0x7fff0000LL / N && T <= (int64_t)0x7fff0000LL / Groups(F_out, N).n;
+  // rows of S, and units (a group has 32 fields at least), within 31 bits
+  return T <= (int64_t)0x7fff0000LL / N && T <= (int64_t)0x7fff0000LL / ((F_out + kCoStep - 1) / kCoStep);
 }
 
 #define EQLIN_CASES                                                                              \
