@@ -141,16 +141,21 @@ def measured_peaks():
 
 
 WGRAD_SOURCES = ("wgrad_tc.cu", "simt_wgrad.cu", "wgrad_noalloc.cu")
+# sources of layers that no pass here runs
+UNTIMED_SOURCES = ("activations.cuh", "dft_pairs.cuh", "gated_", "group_norm.cu")
 
 
 def kernel_source_hash(weight_grad=False):
     """Hash of the sources under csrc (kernels and their host launches) that a
-    pass runs: every file for the weight gradient, every file but the weight
-    gradient's own for the other passes.  A recorded ncu traffic figure holds
+    pass runs: every file but those of the layers not timed here for the weight
+    gradient, and of them every file but the weight gradient's own for the other
+    passes.  A recorded ncu traffic figure holds
     only while its hash is unchanged."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, KERNEL_SOURCES_DIR)
     for name in sorted(os.listdir(d)):
+        if name.startswith(UNTIMED_SOURCES):
+            continue
         if name.endswith((".cu", ".cuh", ".h")) and (weight_grad or name not in WGRAD_SOURCES):
             h.update(name.encode())
             h.update(open(os.path.join(d, name), "rb").read())

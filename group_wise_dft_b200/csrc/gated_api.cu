@@ -30,50 +30,80 @@ int check_call(int64_t T, int N, int Cin, int H, int act, int path) {
 size_t elem_size(int dtype) { return dtype == EQLIN_F32 ? 4 : 2; }
 
 // A spectrum buffer: the fp32 half spectrum Ws[i][c][o] of the CUDA-core kernels,
-// then, for the layers that have a tensor-core form, its packed weights.  The
-// forward's is the layer Cin -> 2H (rows (j, 0), (j, 1)), the adjoint 2H -> Cin.
+// then, for the layers that have tensor-core forms, their packed weights: the
+// two-pass products', and for a gated layer that fits it the fused C_8 kernel's.
+// The forward's layer is Cin -> 2H (rows (j, 0), (j, 1)), the adjoint's 2H -> Cin.
 struct SpecLayout {
-  size_t tc_offset, tc_bytes, total;
+  size_t gemm, fused, total;   // byte offsets; gemm = 0, fused = 0: no such section
 };
-SpecLayout layout(int N, int F_in, int F_out, size_t tc_bytes) {
-  SpecLayout L;
-  L.tc_offset = round256((size_t)F_in * N * F_out * sizeof(float));
-  L.tc_bytes = tc_bytes;
-  L.total = L.tc_offset + tc_bytes;
+SpecLayout layout(int N, int F_in, int F_out, bool gemm, bool fused) {
+  SpecLayout L{};
+  L.total = round256((size_t)F_in * N * F_out * sizeof(float));
+  if (gemm) {
+    L.gemm = L.total;
+    L.total += round256(gemm_tc_bytes(N, F_in, F_out));
+  }
+  if (fused) {
+    L.fused = L.total;
+    L.total += round256(cyclic_tc_bytes(N, F_in, F_out));
+  }
   return L;
 }
-// The fused C_8 kernel where its shapes fit, the two-pass products for the rest
-// of the 16-bit layers.
-enum Tc { kTcNone, kTcFused, kTcGemm };
-Tc tc_kind(int N, int Cin, int H, int dtype) {
-  if (cyclic_tc_supported(N, Cin, 2 * H, dtype) || cyclic_tc_f16_supported(N, Cin, 2 * H, dtype)) return kTcFused;
-  return gemm_tc_supported(N, Cin, 2 * H, dtype) && gemm_tc_supported(N, 2 * H, Cin, dtype) ? kTcGemm : kTcNone;
+bool fused_supported(int N, int Cin, int H, int dtype) {
+  return cyclic_tc_supported(N, Cin, 2 * H, dtype) || cyclic_tc_f16_supported(N, Cin, 2 * H, dtype);
+}
+bool tc_supported(int N, int Cin, int H, int dtype) {
+  return gemm_tc_supported(N, Cin, 2 * H, dtype) && gemm_tc_supported(N, 2 * H, Cin, dtype);
 }
 SpecLayout spec_layout(int N, int Cin, int H, int dtype) {
-  const Tc k = tc_kind(N, Cin, H, dtype);
-  return layout(N, Cin, 2 * H, k == kTcFused ? cyclic_tc_bytes(N, Cin, 2 * H) : k == kTcGemm ? gemm_tc_bytes(N, Cin, 2 * H) : 0);
-}
-SpecLayout contract_layout(int N, int H, int Cout, int dtype) {
-  return layout(N, H, Cout, gemm_tc_supported(N, H, Cout, dtype) ? gemm_tc_bytes(N, H, Cout) : 0);
+  const bool tc = tc_supported(N, Cin, H, dtype);
+  return layout(N, Cin, 2 * H, tc, tc && fused_supported(N, Cin, H, dtype));
 }
 SpecLayout adjoint_layout(int N, int Cin, int H, int dtype) {
-  return layout(N, 2 * H, Cin, tc_kind(N, Cin, H, dtype) != kTcNone ? gemm_tc_bytes(N, 2 * H, Cin) : 0);
+  return layout(N, 2 * H, Cin, tc_supported(N, Cin, H, dtype), false);
+}
+SpecLayout contract_layout(int N, int H, int Cout, int dtype) {
+  return layout(N, H, Cout, gemm_tc_supported(N, H, Cout, dtype), false);
 }
 const float *fp32_section(const void *spec) { return static_cast<const float *>(spec); }
-const void *tc_section(const void *spec, const SpecLayout &L) { return static_cast<const char *>(spec) + L.tc_offset; }
+const void *section(const void *spec, size_t offset) { return static_cast<const char *>(spec) + offset; }
 
-// Few tokens go to the CUDA cores: they spread the weights' reading over the
-// whole GPU, where one tile of the tensor-core kernels would keep a single pair
-// of SMs busy.
-constexpr int64_t kTcTokensLeast = 33;
-Tc tc_for(int64_t T, int N, int Cin, int H, int dtype, int path) {
-  const Tc k = tc_kind(N, Cin, H, dtype);
-  if (path == EQLIN_PATH_SIMT || !gemm_tc_tokens_ok(T, N, Cin > 2 * H ? Cin : 2 * H)) return kTcNone;
-  if (path == EQLIN_PATH_AUTO && (dtype != EQLIN_BF16 || T < kTcTokensLeast)) return kTcNone;
-  return k;
+// Which form a call takes, by measured times on a B200 (bf16, one launch sequence
+// in a CUDA graph; us).
+//
+// Tensor cores or CUDA cores: by the call's products per bin, T Cin 2H (2N - 2).
+// The two-pass form costs about 9 to 14 us however few they are; the CUDA cores'
+// few-token kernel spreads the weights' reading over the whole GPU and wins below
+// about 2^24 (forward, Cin -> H, N, T: 60 -> 160, 12, 32: 9.1 against 10.9 and at 48
+// tokens 18.9 against 10.9; 96 -> 384, 16, 8: 11.0 against 13.6, at 16: 20.1 against
+// 14.6).  The backward's three passes pass that point at 2^22 once there are more
+// tokens than the few-token kernel takes (40 -> 100, 4: 32 tokens 19 against 31, 96
+// tokens 58 against 31; 64 -> 160, 8: 32 tokens 33 against 51, 48 tokens 100 against 52).
+constexpr double kTcProductsForward = 1 << 24, kTcProductsBackward = 1 << 22;
+constexpr int64_t kTcTokensBackward = 33;
+// Fused kernel or two-pass products (N = 8): the fused kernel keeps a token tile on
+// one pair of SMs for all its outputs (160 -> 432: 41 us for one tile as for 74), the
+// other spreads a tile's outputs over the GPU (160 -> 432 forward: 2048 tokens 30 us,
+// 4095 46, where the fused kernel takes 43; 64 -> 160: 12.6, 15.8 and 17.4; backward,
+// 160 -> 432: 4095 tokens 137 against 164, at 8192 about 250 against 209).
+constexpr int64_t kFusedTokensForward = 4096, kFusedTokensBackward = 6144;
+
+enum Tc { kTcNone, kTcFused, kTcGemm };
+Tc tc_for(int64_t T, int N, int Cin, int H, int dtype, int path, bool backward) {
+  if (path == EQLIN_PATH_SIMT || !tc_supported(N, Cin, H, dtype) || !gemm_tc_tokens_ok(T, N, Cin > 2 * H ? Cin : 2 * H))
+    return kTcNone;
+  if (path == EQLIN_PATH_AUTO) {
+    if (dtype != EQLIN_BF16) return kTcNone;
+    const double products = (double)T * Cin * 2.0 * H * (N > 1 ? 2 * N - 2 : 1);
+    if (products < (backward ? kTcProductsBackward : kTcProductsForward)) return kTcNone;
+    if (backward && T < kTcTokensBackward) return kTcNone;
+  }
+  return fused_supported(N, Cin, H, dtype) && T >= (backward ? kFusedTokensBackward : kFusedTokensForward) ? kTcFused
+                                                                                                         : kTcGemm;
 }
+// The forward's workspace where it can take the two-pass form.
 size_t forward_workspace(int64_t T, int N, int Cin, int H, int dtype) {
-  return tc_kind(N, Cin, H, dtype) == kTcGemm ? round256(gemm_tc_spectra_bytes(T, N, Cin)) : 0;
+  return tc_for(T, N, Cin, H, dtype, EQLIN_PATH_TC, false) == kTcGemm ? round256(gemm_tc_spectra_bytes(T, N, Cin)) : 0;
 }
 
 // The backward's workspace.  CUDA cores: dp [T][2H][N] `dtype`, the weight
@@ -97,7 +127,7 @@ BackwardParts tc_parts(int64_t T, int N, int Cin, int H) {
 }
 size_t backward_workspace(int64_t T, int N, int Cin, int H, int dtype) {
   const size_t a = simt_parts(T, N, Cin, H, dtype).total;
-  const size_t b = tc_for(T, N, Cin, H, dtype, EQLIN_PATH_TC) == kTcNone ? 0 : tc_parts(T, N, Cin, H).total;
+  const size_t b = tc_for(T, N, Cin, H, dtype, EQLIN_PATH_TC, true) == kTcNone ? 0 : tc_parts(T, N, Cin, H).total;
   return a > b ? a : b;
 }
 
@@ -110,11 +140,12 @@ int weight_spectrum(const void *W, int N, int Cin, int H, int dtype, bool adjoin
   if (!aligned(W, 16) || !aligned(out, 16)) return set_error(EQLIN_ERR_ALIGN, "W and the spectrum must be 16-byte aligned");
   const SpecLayout L = adjoint ? adjoint_layout(N, Cin, H, dtype) : spec_layout(N, Cin, H, dtype);
   if (bytes < L.total) return set_error(EQLIN_ERR_SIZE, "spectrum buffer of %zu bytes < required %zu", bytes, L.total);
-  if (L.tc_bytes) {
-    char *tc = static_cast<char *>(out) + L.tc_offset;
-    if (adjoint) return launch_gemm_tc_pack(W, N, 2 * H, Cin, true, dtype, out, tc, s);
-    return tc_kind(N, Cin, H, dtype) == kTcFused ? launch_gated_tc_pack(W, Cin, 2 * H, dtype, out, tc, s)
-                                                 : launch_gemm_tc_pack(W, N, Cin, 2 * H, false, dtype, out, tc, s);
+  char *base = static_cast<char *>(out);
+  if (L.gemm) {
+    rc = adjoint ? launch_gemm_tc_pack(W, N, 2 * H, Cin, true, dtype, out, base + L.gemm, s)
+                 : launch_gemm_tc_pack(W, N, Cin, 2 * H, false, dtype, out, base + L.gemm, s);
+    if (!rc && L.fused) rc = launch_gated_tc_pack(W, Cin, 2 * H, dtype, base + L.fused, s);
+    return rc;
   }
   CyclicSpecLayout C{};   // the fp32 section alone
   return adjoint ? launch_cyclic_spectrum(W, N, 2 * H, Cin, dtype, 1, out, C, s)
@@ -172,7 +203,7 @@ int eqlin_cyclic_gated_weight_spectrum_adjoint(const void *W, int N, int Cin, in
 
 int eqlin_cyclic_gated_auto_path(int N, int Cin, int H, int dtype) {
   if (check_shape(N, Cin, H, dtype) != EQLIN_OK) return -1;
-  return tc_kind(N, Cin, H, dtype) != kTcNone && dtype == EQLIN_BF16 ? EQLIN_PATH_TC : EQLIN_PATH_SIMT;
+  return tc_supported(N, Cin, H, dtype) && dtype == EQLIN_BF16 ? EQLIN_PATH_TC : EQLIN_PATH_SIMT;
 }
 
 size_t eqlin_cyclic_gated_forward_workspace_bytes(int64_t T, int N, int Cin, int H, int dtype) {
@@ -187,26 +218,28 @@ int eqlin_cyclic_gated_forward(const void *x, const void *Wspec, void *h, int64_
   clear_error();
   int rc = check_shape(N, Cin, H, dtype);
   if (rc || (rc = check_call(T, N, Cin, H, act, path))) return rc;
-  if (path == EQLIN_PATH_TC && tc_for(T, N, Cin, H, dtype, path) == kTcNone)
+  if (path == EQLIN_PATH_TC && tc_for(T, N, Cin, H, dtype, path, false) == kTcNone)
     return set_error(EQLIN_ERR_UNSUPPORTED, "%s", kTcNeeds);
   if (T == 0) return EQLIN_OK;
   if (!x || !Wspec || !h) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
   if (!aligned(x, 16) || !aligned(h, 16) || !aligned(Wspec, 16))
     return set_error(EQLIN_ERR_ALIGN, "x, h and Wspec must be 16-byte aligned");
   const cudaStream_t s = (cudaStream_t)stream;
-  Tc k = tc_for(T, N, Cin, H, dtype, path);
+  Tc k = tc_for(T, N, Cin, H, dtype, path, false);
   if (k == kTcGemm) {
     const size_t need = forward_workspace(T, N, Cin, H, dtype);
-    const bool ok = workspace && workspace_bytes >= need && aligned(workspace, 256);
-    if (!ok && path == EQLIN_PATH_TC)
-      return set_error(EQLIN_ERR_SIZE, "this tensor-core path needs a 256-byte aligned workspace of %zu bytes", need);
-    if (!ok) k = kTcNone;
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) {
+      if (path == EQLIN_PATH_TC)
+        return set_error(EQLIN_ERR_SIZE, "this tensor-core path needs a 256-byte aligned workspace of %zu bytes", need);
+      k = fused_supported(N, Cin, H, dtype) ? kTcFused : kTcNone;
+    }
   }
-  const void *pack = tc_section(Wspec, spec_layout(N, Cin, H, dtype));
-  if (k == kTcFused) return launch_gated_tc(kEpiGated, x, pack, nullptr, h, T, Cin, 2 * H, act, dtype, s);
+  const SpecLayout L = spec_layout(N, Cin, H, dtype);
+  if (k == kTcFused)
+    return launch_gated_tc(kEpiGated, x, section(Wspec, L.fused), nullptr, h, T, Cin, 2 * H, act, dtype, s);
   if (k == kTcGemm) {
     if ((rc = launch_gemm_tc_spectra(x, workspace, T, N, Cin, dtype, s))) return rc;
-    return launch_gemm_tc(kEpiGated, workspace, pack, nullptr, h, T, N, Cin, 2 * H, act, dtype, s);
+    return launch_gemm_tc(kEpiGated, workspace, section(Wspec, L.gemm), nullptr, h, T, N, Cin, 2 * H, act, dtype, s);
   }
   GatedIo io{};
   io.x = x;
@@ -232,7 +265,7 @@ int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec
   const cudaStream_t s = (cudaStream_t)stream;
   int rc = check_shape(N, Cin, H, dtype);
   if (rc || (rc = check_call(T, N, Cin, H, act, path))) return rc;
-  if (path == EQLIN_PATH_TC && tc_for(T, N, Cin, H, dtype, path) == kTcNone)
+  if (path == EQLIN_PATH_TC && tc_for(T, N, Cin, H, dtype, path, false) == kTcNone)
     return set_error(EQLIN_ERR_UNSUPPORTED, "%s", kTcNeeds);
   if (!dx && !dW) return set_error(EQLIN_ERR_INVALID_ARG, "dx and dW are both null");
   if (!aligned(dW, 16)) return set_error(EQLIN_ERR_ALIGN, "dW must be 16-byte aligned");
@@ -249,21 +282,22 @@ int eqlin_cyclic_gated_backward(const void *x, const void *dh, const void *Wspec
   if (workspace_bytes < need) return set_error(EQLIN_ERR_SIZE, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
   if (!aligned(workspace, 256)) return set_error(EQLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
   char *ws = static_cast<char *>(workspace);
-  const Tc k = tc_for(T, N, Cin, H, dtype, path);
+  const Tc k = tc_for(T, N, Cin, H, dtype, path, true);
   if (k != kTcNone) {
     const BackwardParts p = tc_parts(T, N, Cin, H);
     void *Sdp = ws, *Sx = ws + p.x;
-    const void *pack = tc_section(Wspec, spec_layout(N, Cin, H, dtype));
+    const SpecLayout L = spec_layout(N, Cin, H, dtype);
     // the columns past dp's last field are read too
     if (spectra_width(2 * H) != 2 * H && cudaMemsetAsync(Sdp, 0, p.x, s) != cudaSuccess)
       return check_launch("gated layer backward (spectra)");
     if (k == kTcGemm || dW) {
       if ((rc = launch_gemm_tc_spectra(x, Sx, T, N, Cin, dtype, s))) return rc;
     }
-    rc = k == kTcFused ? launch_gated_tc(kEpiGates, x, pack, dh, Sdp, T, Cin, 2 * H, act, dtype, s)
-                       : launch_gemm_tc(kEpiGates, Sx, pack, dh, Sdp, T, N, Cin, 2 * H, act, dtype, s);
+    rc = k == kTcFused
+             ? launch_gated_tc(kEpiGates, x, section(Wspec, L.fused), dh, Sdp, T, Cin, 2 * H, act, dtype, s)
+             : launch_gemm_tc(kEpiGates, Sx, section(Wspec, L.gemm), dh, Sdp, T, N, Cin, 2 * H, act, dtype, s);
     if (!rc && dx)
-      rc = launch_gemm_tc(kEpiLinear, Sdp, tc_section(Wspec_adj, adjoint_layout(N, Cin, H, dtype)), nullptr, dx, T, N,
+      rc = launch_gemm_tc(kEpiLinear, Sdp, section(Wspec_adj, adjoint_layout(N, Cin, H, dtype).gemm), nullptr, dx, T, N,
                           2 * H, Cin, EQLIN_ACT_NONE, dtype, s);
     if (!rc && dW)
       rc = launch_gemm_tc_wgrad(Sx, Sdp, dW, T, N, Cin, 2 * H, dtype, reinterpret_cast<float *>(ws + p.part), s);
@@ -310,8 +344,8 @@ int eqlin_cyclic_gated_mlp_contract_spectrum(const void *W, int N, int H, int Ci
   const SpecLayout L = contract_layout(N, H, Cin, dtype);
   if (Wspec_bytes < L.total)
     return set_error(EQLIN_ERR_SIZE, "spectrum buffer of %zu bytes < required %zu", Wspec_bytes, L.total);
-  if (L.tc_bytes)
-    return launch_gemm_tc_pack(W, N, H, Cin, false, dtype, Wspec, static_cast<char *>(Wspec) + L.tc_offset,
+  if (L.gemm)
+    return launch_gemm_tc_pack(W, N, H, Cin, false, dtype, Wspec, static_cast<char *>(Wspec) + L.gemm,
                                (cudaStream_t)stream);
   CyclicSpecLayout C{};   // the fp32 section alone
   return launch_cyclic_spectrum(W, N, H, Cin, dtype, 0, Wspec, C, (cudaStream_t)stream);
@@ -332,7 +366,7 @@ int eqlin_cyclic_gated_mlp(const void *x, const void *gamma, const void *beta, c
   if (rc || (rc = check_call(T, N, Cin, H, act, path))) return rc;
   if (G < 0 || (G > 0 && Cin % G != 0))
     return set_error(EQLIN_ERR_INVALID_ARG, "Cin=%d must be a multiple of G=%d groups (0: no norm)", Cin, G);
-  Tc k = tc_for(T, N, Cin, H, dtype, path);
+  const Tc k = tc_for(T, N, Cin, H, dtype, path, false);
   if (path == EQLIN_PATH_TC && (k == kTcNone || !gemm_tc_supported(N, H, Cin, dtype)))
     return set_error(EQLIN_ERR_UNSUPPORTED, "%s", kTcNeeds);
   if (T == 0) return EQLIN_OK;
@@ -358,7 +392,7 @@ int eqlin_cyclic_gated_mlp(const void *x, const void *gamma, const void *beta, c
   if (rc) return rc;
   if (k != kTcNone && gemm_tc_supported(N, H, Cin, dtype)) {
     if ((rc = launch_gemm_tc_spectra(hidden, scratch, T, N, H, dtype, s))) return rc;
-    return launch_gemm_tc(kEpiLinear, scratch, tc_section(W2spec, contract_layout(N, H, Cin, dtype)), nullptr, y, T, N,
+    return launch_gemm_tc(kEpiLinear, scratch, section(W2spec, contract_layout(N, H, Cin, dtype).gemm), nullptr, y, T, N,
                           H, Cin, EQLIN_ACT_NONE, dtype, s);
   }
   GatedIo io{};

@@ -42,9 +42,9 @@ inline int launch_gated_simt(int epi, const GatedIo &io, int N, int act, int dty
 
 // Tensor-core form for C_8, bf16 and fp16 (spectral_tc.cu): kEpiGated or
 // kEpiGates of the layer Cin -> Cout = 2H (Cin and H multiples of 16, Cin <= 160)
-// from the packed weight stages Bpack (cyclic_tc_bytes), written by
-// launch_gated_tc_pack beside the fp32 spectrum Ws.
-int launch_gated_tc_pack(const void *W, int Cin, int Cout, int dtype, void *Ws, void *dst, cudaStream_t s);
+// from the packed weight stages Bpack (cyclic_tc_bytes) that launch_gated_tc_pack
+// writes.
+int launch_gated_tc_pack(const void *W, int Cin, int Cout, int dtype, void *dst, cudaStream_t s);
 int launch_gated_tc(int epi, const void *x, const void *Bpack, const void *dh, void *out, int64_t T, int Cin,
                     int Cout, int act, int dtype, cudaStream_t s);
 

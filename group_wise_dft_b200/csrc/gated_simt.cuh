@@ -351,8 +351,10 @@ spectral_few_kernel(const T *__restrict__ x, const float *__restrict__ Ws, const
   }
 }
 
-// Tokens up to which the few-token kernel runs.
-constexpr int64_t kFewTokensMost = 32;
+// Tokens up to which the few-token kernel runs.  Its time grows with them, the tile
+// kernel's does not until the tiles fill the GPU (us, fp32, at 32 tokens: 40 -> 100,
+// C_4: 3.1 against 7.4; 160 -> 432, C_8: 20 against 32; 96 -> 384, C_16: 38 against 38).
+template <int N> constexpr int64_t few_tokens_most() { return N <= 8 ? 48 : 32; }
 
 // Fewer full tiles than half the SMs go as small ones.
 constexpr int64_t kTileCtasLeast = 74;
@@ -376,7 +378,7 @@ int launch_tiles(const GatedIo &io, int act, const DftTables &tab, cudaStream_t 
 
 template <int N, typename T, int EPI>
 int launch_ne(const GatedIo &io, int act, const DftTables &tab, cudaStream_t s) {
-  if (io.T <= kFewTokensMost) {
+  if (io.T <= few_tokens_most<N>()) {
     const dim3 grid((unsigned)((io.Cout + kFewOut - 1) / kFewOut),
                     (unsigned)((io.T + few_tokens<N>() - 1) / few_tokens<N>()));
     spectral_few_kernel<N, T, EPI><<<grid, kThreads, 0, s>>>((const T *)io.x, io.Ws, (const T *)io.dh,

@@ -900,13 +900,14 @@ int make_shape(int64_t B, int64_t S, int F, int N, int G, int dtype, GnShape *ou
     // positions and the fixed part; at least 4 positions per thread
     const Tiling tl = col_tiling(sh);
     const int64_t most = (S + 4 * tl.lanes - 1) / (4 * tl.lanes), row = (int64_t)sh.L * elem_size(dtype);
-    const int64_t tries = 8 * kChunkResident / B + 1;
     int64_t best = 1;
-    double least = 0.0;
-    for (int64_t c = 1; c <= most && c <= tries; ++c) {
+    double least = -1.0;
+    for (int64_t full = 1; full <= 8; ++full) {   // as many chunks as fill `full` rounds
+      int64_t c = full * kChunkResident / B;
+      c = c < 1 ? 1 : (c > most ? most : c);
       const int64_t rounds = (B * c + kChunkResident - 1) / kChunkResident;
       const double cost = (double)rounds * ((double)((S + c - 1) / c) * (double)row + (double)kChunkFixed);
-      if (c == 1 || cost < least) {
+      if (least < 0.0 || cost < least) {
         least = cost;
         best = c;
       }

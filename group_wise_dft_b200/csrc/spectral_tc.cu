@@ -1471,11 +1471,11 @@ __global__ void pack_b_kernel(const void *__restrict__ Wc, D8Blocks d8, int F_in
 // whole in one launch and in fp32 (a training step packs its weights anew each
 // time: one launch per chunk with 64-bit twiddles per element took 0.3 ms at 160
 // -> 864 fields): one thread per (output field, 8 input fields) computes their
-// half spectra and writes one 16-byte run per panel row, and the fp32 section
-// Ws[i][c][o] of the CUDA-core kernels.  Lanes walk the output fields.
+// half spectra and writes one 16-byte run per panel row.  Lanes walk the output
+// fields.
 template <bool H>
 __global__ void __launch_bounds__(256)
-pack_c8_kernel(const uint4 *__restrict__ W, int F_in, int F_out, float *__restrict__ Ws, uint8_t *__restrict__ dst) {
+pack_c8_kernel(const uint4 *__restrict__ W, int F_in, int F_out, uint8_t *__restrict__ dst) {
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= (int64_t)F_out * (F_in / 8)) return;
   const int o = (int)(idx % F_out), ib = (int)(idx / F_out);
@@ -1488,10 +1488,7 @@ pack_c8_kernel(const uint4 *__restrict__ W, int F_in, int F_out, float *__restri
     fwd_cyclic8(x, z);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float2 v = scl2(z[c], 0.125f);
-      Ws[((size_t)i * 8 + c) * F_out + o] = v.x;
-      Ws[((size_t)(i + 1) * 8 + c) * F_out + o] = v.y;
-      const float2 t = c == 0 || c == 7 ? v : scl2(v, 2.0f);   // the one-sided inverse's factor
+      const float2 t = scl2(z[c], c == 0 || c == 7 ? 0.125f : 0.25f);   // with the one-sided inverse's factor
       out[c][p] = pack_x2<H>(t.x, t.y);
     }
   }
@@ -1899,15 +1896,14 @@ int launch_cyclic_tc_f32(const void *x, const void *Bpack, void *y, int64_t T, i
   return EQLIN_OK;
 }
 
-int launch_gated_tc_pack(const void *W, int Cin, int Cout, int dtype, void *Ws, void *dst, cudaStream_t s) {
+int launch_gated_tc_pack(const void *W, int Cin, int Cout, int dtype, void *dst, cudaStream_t s) {
   const int64_t n = (int64_t)Cout * (Cin / 8);
   const unsigned grid = (unsigned)((n + 255) / 256);
+  const uint4 *w = static_cast<const uint4 *>(W);
   if (dtype == EQLIN_F16)
-    pack_c8_kernel<true><<<grid, 256, 0, s>>>(static_cast<const uint4 *>(W), Cin, Cout, static_cast<float *>(Ws),
-                                              static_cast<uint8_t *>(dst));
+    pack_c8_kernel<true><<<grid, 256, 0, s>>>(w, Cin, Cout, static_cast<uint8_t *>(dst));
   else
-    pack_c8_kernel<false><<<grid, 256, 0, s>>>(static_cast<const uint4 *>(W), Cin, Cout, static_cast<float *>(Ws),
-                                               static_cast<uint8_t *>(dst));
+    pack_c8_kernel<false><<<grid, 256, 0, s>>>(w, Cin, Cout, static_cast<uint8_t *>(dst));
   return check_launch("gated layer weight packing");
 }
 

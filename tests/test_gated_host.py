@@ -94,7 +94,7 @@ def test_forward_workspace():
     """Some tensor-core shapes need one; they are refused without it when asked for."""
     need = L.eqlin_cyclic_gated_forward_workspace_bytes(100, 16, 96, 64, eq.EQLIN_BF16)
     assert need >= 100 * 96 * 16 * 2 and need % 256 == 0
-    assert L.eqlin_cyclic_gated_forward_workspace_bytes(100, 8, 96, 64, eq.EQLIN_BF16) == 0
+    assert L.eqlin_cyclic_gated_forward_workspace_bytes(100000, 8, 96, 64, eq.EQLIN_BF16) == 0
     assert L.eqlin_cyclic_gated_forward_workspace_bytes(100, 16, 96, 64, eq.EQLIN_F32) == 0
     tc = dict(T=100, N=16, C=96, H=64, dtype=eq.EQLIN_BF16, path=eq.PATH_TC)
     assert fwd(**tc) == eq.EQLIN_ERR_SIZE

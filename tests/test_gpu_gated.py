@@ -114,18 +114,20 @@ def test_cuda_cores(T, C, H, N, act, dtype):
     run(T, C, H, N, dtype, act, path=eq.PATH_SIMT)
 
 
-# tensor cores: ragged tiles, one 32-field chunk or several, output groups of dx with padding (Cin = 16, 48, ..),
-# several tiles per pair of CTAs
+# tensor cores, C_8: ragged tiles, one 32-field chunk or several, output groups of dx with padding (Cin = 16, 48, ..);
+# from 4096 tokens (backward: 6144) on the fused kernel, several tiles per pair of CTAs
 TC = [
     (33, 16, 16, "silu"), (64, 32, 48, "gelu"), (127, 48, 16, "none"), (128, 80, 64, "silu"), (129, 112, 80, "gelu"),
     (300, 160, 432, "silu"), (1000, 144, 96, "gelu"), (3 * 74 * 128 + 77, 32, 32, "silu"),
     (2 * 74 * 128 + 1, 160, 48, "silu"), (20000, 96, 160, "gelu"),
+    (4096, 48, 64, "gelu"), (6200, 160, 432, "none"), (4095, 160, 432, "silu"),
 ]
 
 
 @pytest.mark.parametrize("T,C,H,act", TC)
 def test_tensor_cores(T, C, H, act):
     assert eq.cyclic_gated_auto_path(8, C, H, BF16) == eq.PATH_TC
+    run(T, C, H, 8, BF16, act, path=eq.PATH_TC, halves=(2, 2.5, 2.5))
     run(T, C, H, 8, BF16, act, halves=(2, 2.5, 2.5))
 
 
@@ -133,6 +135,7 @@ def test_tensor_cores(T, C, H, act):
 def test_tensor_cores_when_asked_for(T, C, H, act):
     """fp16, and bf16 for a handful of tokens."""
     run(T, C, H, 8, F16, act, path=eq.PATH_TC, halves=(2, 2.5, 2.5))
+    run(T + 6144, C, H, 8, F16, act, path=eq.PATH_TC, halves=(2, 2.5, 2.5))
     run(T % 32 + 1, C, H, 8, BF16, act, path=eq.PATH_TC, halves=(2, 2.5, 2.5))
 
 
@@ -166,6 +169,18 @@ def test_outputs_at_odd_addresses():
     eq.cyclic_gated_backward(x, dh, spec, adj, dx=dx, dW=dW)
     near(dx, rdx, 2.5)
     near(dW, rdW, 2.5)
+
+
+def test_without_a_workspace():
+    """AUTO then takes a form that needs none: the fused kernel, or the CUDA cores."""
+    L, s = eq.raw_lib(), torch.cuda.current_stream().cuda_stream
+    for T, C, H, N in ((300, 160, 432, 8), (300, 96, 130, 16)):
+        x, W, _ = tensors(T, C, H, N, BF16, 12)
+        spec, h = eq.cyclic_gated_weight_spectrum(W), torch.full((T, H, N), float("nan"), dtype=BF16, device="cuda")
+        args = (x.data_ptr(), spec.data_ptr(), h.data_ptr(), T, N, C, H, eq.ACT_SILU, eq.EQLIN_BF16)
+        assert L.eqlin_cyclic_gated_forward(*args, eq.PATH_AUTO, None, 0, s) == 0
+        near(h, reference(x, W, "silu"), 2)
+        assert L.eqlin_cyclic_gated_forward(*args, eq.PATH_TC, None, 0, s) == eq.EQLIN_ERR_SIZE
 
 
 def test_no_tokens():
