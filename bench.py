@@ -147,10 +147,9 @@ UNTIMED_SOURCES = ("activations.cuh", "dft_pairs.cuh", "gated_", "group_norm.cu"
 
 def kernel_source_hash(weight_grad=False):
     """Hash of the sources under csrc (kernels and their host launches) that a
-    pass runs: every file but those of the layers not timed here for the weight
-    gradient, and of them every file but the weight gradient's own for the other
-    passes.  A recorded ncu traffic figure holds
-    only while its hash is unchanged."""
+    pass runs: every file but those of the layers not timed here; for the passes
+    other than the weight gradient also without that one's own.  A recorded ncu
+    traffic figure holds only while its hash is unchanged."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, KERNEL_SOURCES_DIR)
     for name in sorted(os.listdir(d)):

@@ -368,7 +368,7 @@ int eqlin_cyclic_gated_mlp(const void *x, const void *gamma, const void *beta, c
     return set_error(EQLIN_ERR_INVALID_ARG, "Cin=%d must be a multiple of G=%d groups (0: no norm)", Cin, G);
   const Tc k = tc_for(T, N, Cin, H, dtype, path, false);
   if (path == EQLIN_PATH_TC && (k == kTcNone || !gemm_tc_supported(N, H, Cin, dtype)))
-    return set_error(EQLIN_ERR_UNSUPPORTED, "%s", kTcNeeds);
+    return set_error(EQLIN_ERR_UNSUPPORTED, "the block's tensor-core path needs bf16 or fp16, Cin >= 16 and H >= 16");
   if (T == 0) return EQLIN_OK;
   if (!x || !W1spec || !W2spec || !y) return set_error(EQLIN_ERR_INVALID_ARG, "null pointer");
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(W1spec, 16) || !aligned(W2spec, 16))

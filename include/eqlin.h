@@ -1,8 +1,8 @@
 /*
  * eqlin.h -- C ABI of the B200 equivariant linear layers.
  *
- * Two layers, both mapping a batch of T tokens in the regular representation
- * of a finite group to another such batch:
+ * Layers that map a batch of T tokens in the regular representation of a
+ * finite group to another such batch:
  *
  *  1. Cyclic EQ-Linear over C_N ("Flash EQ-Linear: Accelerating Equivariant
  *     Linear Layers via Group-wise Discrete Fourier Transform",
@@ -21,6 +21,10 @@
  *     A1, A2, B1, B2, E, four (C/8)-square products, one (C/4)-square product
  *     shared by E's two row coordinates, the change of basis back, and an
  *     optional GELU in the regular domain.
+ *
+ *  3. What stands around them in a transformer or a convolutional network: the
+ *     group norm with an activation, the gated feed-forward layer over C_N (both
+ *     with their backward passes), and the pre-norm gated feed-forward block.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -369,7 +373,8 @@ EQLIN_API int eqlin_d8_fourier_mlp(const void *z, const void *W1pack, const void
  * eqlin_cyclic_gated_backward: the gradients of sum(dh * h).  p is computed
  * again (the forward keeps nothing), then
  *     dp[t, j, 0] = dh p[t, j, 1] act'(p[t, j, 0]),  dp[t, j, 1] = dh act(p[t, j, 0])
- * go, rounded to `dtype`, to the workspace, and from them
+ * go to the workspace rounded to `dtype` (on CUDA cores dp itself, on tensor cores
+ * its half spectra, from fp32 values of dp), and from them
  *     dx[t, i, h] = sum_j sum_a sum_g W[j, a, i, (g - h) mod N] dp[t, j, a, g],
  *     dW[j, a, i, m] = sum_t sum_g dp[t, j, a, g] x[t, i, (g - m) mod N].
  * dh: device [T][H][N]; dx: device [T][Cin][N]; dW: device [H][2][Cin][N]
@@ -384,10 +389,16 @@ EQLIN_API int eqlin_d8_fourier_mlp(const void *z, const void *W1pack, const void
  * CUDA cores in fp32; EQLIN_PATH_TC, on tensor cores, for bf16 and fp16 with
  * Cin >= 16 and H >= 8 (EQLIN_ERR_UNSUPPORTED otherwise): the half spectra of x,
  * W and dp are rounded to `dtype` (fp16: sums of N values of x must not overflow
- * it), fp32 accumulation.  AUTO takes the tensor cores for bf16 and more than a
- * handful of tokens.  The forward needs a workspace on some of those shapes
- * (eqlin_cyclic_gated_forward_workspace_bytes, 0 elsewhere); without it AUTO runs on
- * CUDA cores and EQLIN_PATH_TC returns EQLIN_ERR_SIZE. */
+ * it), fp32 accumulation.  AUTO takes the tensor cores for bf16 where the call has
+ * enough products to gain by it (eqlin_cyclic_gated_auto_path: TC where some number
+ * of tokens does); fp16 and fp32 stay on CUDA cores.
+ * On tensor cores a call runs as one fused kernel (N = 8, Cin and H multiples of
+ * 16, Cin <= 160, thousands of tokens) or as x's half spectra and then products
+ * over them; the forward of the second form needs the workspace
+ * (eqlin_cyclic_gated_forward_workspace_bytes, 0 where no path of the call needs
+ * one).  Without it, or with one that is too small or not aligned, AUTO runs the
+ * fused kernel where the shape has it and CUDA cores elsewhere, and
+ * EQLIN_PATH_TC returns EQLIN_ERR_SIZE. */
 EQLIN_API size_t eqlin_cyclic_gated_spectrum_bytes(int N, int Cin, int H, int dtype);
 EQLIN_API int eqlin_cyclic_gated_weight_spectrum(const void *W, int N, int Cin, int H, int dtype, void *Wspec,
                                        size_t Wspec_bytes, eqlin_stream_t stream);
@@ -441,14 +452,15 @@ EQLIN_API int eqlin_group_norm_backward(const void *x, const void *dy, const flo
 
 /* The feed-forward block of a pre-norm transformer over C_N, forward:
  *     y = contract(gated(norm(x))),
- * norm the token group norm above (S = 1, G groups, no activation; G = 0: none),
+ * norm the token group norm above (S = 1, G groups, no activation; G = 0: none, and
+ * gamma and beta are not read),
  * gated the gated layer Cin -> H (W1spec from eqlin_cyclic_gated_weight_spectrum),
  * contract the cyclic layer H -> Cin of W2, device [Cin][H][N], any H (W2spec from
  * eqlin_cyclic_gated_mlp_contract_spectrum, of at least ..._contract_bytes).  x, y:
  * device [T][Cin][N]; gamma, beta as in eqlin_group_norm.  The residual is the
  * caller's to add.  The intermediate values are rounded to `dtype`; they live in
  * the workspace (256-byte aligned, at least ..._workspace_bytes).  Paths as in
- * eqlin_cyclic_gated_forward. */
+ * eqlin_cyclic_gated_forward, but EQLIN_PATH_TC needs H >= 16. */
 EQLIN_API size_t eqlin_cyclic_gated_mlp_contract_bytes(int N, int H, int Cin, int dtype);
 EQLIN_API int eqlin_cyclic_gated_mlp_contract_spectrum(const void *W, int N, int H, int Cin, int dtype, void *Wspec,
                                              size_t Wspec_bytes, eqlin_stream_t stream);
