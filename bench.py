@@ -142,7 +142,7 @@ def measured_peaks():
 
 WGRAD_SOURCES = ("wgrad_tc.cu", "simt_wgrad.cu", "wgrad_noalloc.cu")
 # sources of layers that no pass here runs
-UNTIMED_SOURCES = ("activations.cuh", "dft_pairs.cuh", "gated_", "group_norm.cu")
+UNTIMED_SOURCES = ("activations.cuh", "dft_pairs.cuh", "gated_", "group_norm")
 
 
 def kernel_source_hash(weight_grad=False):

@@ -1,0 +1,991 @@
+// Group norm with a pointwise activation, channels last, forward and backward.
+//
+// x[B][S][F][N]: B items of S positions, F fields of N group slots, the slot
+// fastest.  The F fields form G groups of F / G; per (item b, group g)
+//     mean = E[x],  var = E[(x - mean)^2]   over the S (F/G) N values,
+//     xhat = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),
+//     z = gamma_f xhat + beta_f,  y = act(z).
+// gamma and beta are constant along the group axis, the statistics do not
+// change when the slots are permuted and act is pointwise in the regular
+// domain, so the layer commutes with the group (C_N and D8 alike).
+// Backward, with dz = dy act'(z) and n = S (F/G) N:
+//     dbeta_f = sum dz,  dgamma_f = sum dz xhat,
+//     dx = rstd (gamma dz - sum(gamma dz) / n - xhat sum(gamma dz xhat) / n).
+//
+// Everything is bound by memory.  Two forms:
+//  - an item of at most 32 kRowVecs vectors (a token, S = 1, or a tiny map) is
+//    one warp's, one of up to 16 times as many a CTA's of 2 to 16: its values stay in registers as they came (packed: more warps
+//    fit, and their loads are what hides the latency), so they are read once, and
+//    the variance is the plain two-pass one;
+//  - larger items are split into chunks of positions.  A CTA walks its chunk
+//    with one thread per vector of channels (memory order, whole lines), a few
+//    positions at a time: their mean and squared deviations are exact two-pass
+//    sums in registers, joined by the pairwise update of Chan, Golub and LeVeque
+//    (no cancellation, whatever the mean).  A second launch joins the chunks and
+//    normalises, the last chunks first: they are still in L2.
+// (Batches of items that fit L2, one's first pass in a launch with the previous
+// one's second, were measured and dropped: a batch of 42 MB saves 7 us of memory
+// reads and costs about 20 us of starting and draining a grid.)
+// Statistics, sums and all arithmetic are fp32; every sum has a fixed order.
+#pragma once
+
+#include "activations.cuh"
+#include "group_norm_internal.cuh"
+#include "tc_transforms.cuh"
+
+namespace eqlin {
+namespace {
+
+template <int BYTES> struct VecOf;
+template <> struct VecOf<16> { typedef uint4 type; };
+template <> struct VecOf<8> { typedef uint2 type; };
+template <> struct VecOf<4> { typedef uint32_t type; };
+template <> struct VecOf<2> { typedef uint16_t type; };
+
+// V consecutive values as they lie in memory, and as pairs of fp32 (with V = 1
+// the second lane is a copy that the sums leave out).
+template <typename T, int V>
+struct Raw {
+  typedef typename VecOf<V * sizeof(T)>::type Q;
+  union {
+    Q q;
+    T e[V];
+  };
+};
+template <int V> constexpr int pairs() { return (V + 1) / 2; }
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T *p) {
+  Raw<T, V> r;
+  r.q = __ldg(reinterpret_cast<const typename Raw<T, V>::Q *>(p));
+  return r;
+}
+// (a last reading: not kept in L2)
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_last(const T *p) {
+  Raw<T, V> r;
+  r.q = __ldcs(reinterpret_cast<const typename Raw<T, V>::Q *>(p));
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V> &r, float2 (&v)[pairs<V>()]) {
+#pragma unroll
+  for (int k = 0; k < pairs<V>(); ++k) v[k] = make_float2(to_f32(r.e[2 * k]), to_f32(r.e[V == 1 ? 0 : 2 * k + 1]));
+}
+// Written past L2's working set.
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T *p, const float2 (&v)[pairs<V>()]) {
+  Raw<T, V> r;
+#pragma unroll
+  for (int k = 0; k < pairs<V>(); ++k) {
+    r.e[2 * k] = from_f32<T>(v[k].x);
+    if (V > 1) r.e[2 * k + 1] = from_f32<T>(v[k].y);
+  }
+  __stcs(reinterpret_cast<typename Raw<T, V>::Q *>(p), r.q);
+}
+template <int V>
+__device__ __forceinline__ float lanes_sum(float2 a) { return V == 1 ? a.x : a.x + a.y; }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// The activations on pairs.  16-bit results take GELU through the paired erf of
+// tc_transforms.cuh (about 2e-6, far below their rounding), fp32 results erff.
+template <typename T>
+__device__ __forceinline__ float2 act_pair(int act, float2 z) {
+  if (act == EQLIN_ACT_SILU) return silu2(z);
+  if (act == EQLIN_ACT_GELU)
+    return sizeof(T) == 2 ? gelu_erf2(z) : make_float2(act_value<EQLIN_ACT_GELU>(z.x), act_value<EQLIN_ACT_GELU>(z.y));
+  return z;
+}
+template <typename T>
+__device__ __forceinline__ float2 slope_pair(int act, float2 z) {
+  float2 a;
+  if (act == EQLIN_ACT_SILU) return silu_slope2(z, a);
+  if (act == EQLIN_ACT_GELU) {
+    if (sizeof(T) == 2) return gelu_slope2(z, a);
+    return make_float2(act_slope<EQLIN_ACT_GELU>(z.x, a.x), act_slope<EQLIN_ACT_GELU>(z.y, a.y));
+  }
+  return both(1.0f);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// gamma (or beta) of the V values at channel offset c0, one per SEG values
+// (SEG divides N and V, so a segment lies within a field).
+template <typename T, int V, int SEG>
+__device__ __forceinline__ void load_affine(const T *p, int c0, int N, float missing, float (&a)[V / SEG]) {
+#pragma unroll
+  for (int k = 0; k < V / SEG; ++k) a[k] = p ? to_f32(__ldg(p + (c0 + k * SEG) / N)) : missing;
+}
+template <int V, int SEG>
+__device__ __forceinline__ float2 affine_pair(const float (&a)[V / SEG], int k) {
+  return make_float2(a[2 * k / SEG], a[(V == 1 ? 0 : 2 * k + 1) / SEG]);
+}
+// Sums of a vector's segments, kept as pairs: of a segment's even and odd values
+// (SEG >= 2), or of two segments of one value each.
+template <int V, int SEG> constexpr int seg_pairs() { return SEG >= 2 ? V / SEG : pairs<V>(); }
+template <int SEG> __device__ __forceinline__ constexpr int seg_at(int k) { return SEG >= 2 ? 2 * k / SEG : k; }
+template <int V, int SEG>
+__device__ __forceinline__ float seg_value(const float2 (&s)[seg_pairs<V, SEG>()], int j) {
+  return SEG >= 2 ? s[j].x + s[j].y : (j % 2 ? s[j / 2].y : s[j / 2].x);
+}
+
+// ------------------------------------------------------------ row kernels
+
+// Per-group sums of one item: part[q] (shared memory, one value per vector of
+// the item) -> out[g] (shared memory).  A team of the W warps' lanes, a power of
+// two up to a warp, walks a group's vectors; `me` counts the item's lanes.
+template <int W>
+__device__ __forceinline__ void group_sums(const float *part, float *out, const GnShape &sh, int me) {
+  const int runv = sh.run / sh.vec, Lv = sh.L / sh.vec;
+  const int count = (int)sh.S * runv;
+  int team = 32;
+  while (team > 1 && team * sh.G > 32 * W) team >>= 1;
+  const int r = me & (team - 1);
+  for (int g0 = 0; g0 < sh.G; g0 += 32 * W / team) {
+    const int g = g0 + me / team;
+    float s = 0.0f;
+    if (g < sh.G)
+      for (int j = r; j < count; j += team) s += part[(j / runv) * Lv + g * runv + j % runv];
+    for (int o = team >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (g < sh.G && r == 0) out[g] = s;
+  }
+}
+
+// The warps of an item: their barrier, and the sums of their values of v and w (each
+// warp's in red[2 W], which the caller alternates between two from call to call).
+template <int W> __device__ __forceinline__ void team_sync() {
+  if constexpr (W == 1)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+template <int W>
+__device__ __forceinline__ void item_sums(float &v, float &w, float *red) {
+  v = warp_sum(v);
+  w = warp_sum(w);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 31) == 0) {
+      red[threadIdx.x >> 5] = v;
+      red[W + (threadIdx.x >> 5)] = w;
+    }
+    __syncthreads();
+    v = w = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      v += red[k];
+      w += red[W + k];
+    }
+  }
+}
+template <int W>
+__device__ __forceinline__ float item_sum(float v, float *red) {
+  v = warp_sum(v);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) v += red[k];
+  }
+  return v;
+}
+
+// Warps of a CTA: one item of W warps, or kRowWarps items of one.
+template <int W> constexpr int row_warps() { return W == 1 ? kRowWarps : W; }
+
+// 128-thread CTAs per SM that the row kernels' registers are held to (what fits without
+// spilling, by what a lane keeps: its vectors, and gamma, beta and their
+// gradients' sums once per segment).
+template <int V, int SEG, int NV> constexpr int row_ctas_per_sm() {
+  return NV == 1 ? 8 : NV <= 3 ? (V / SEG <= 2 ? 8 : V / SEG <= 4 ? 6 : 4) : (V == SEG ? 8 : V / SEG <= 2 ? 6 : 4);
+}
+template <int V, int SEG, int NV> constexpr int row_backward_ctas_per_sm() {
+  return NV == 1 ? 5 : NV <= 3 ? (V == SEG ? 5 : 3) : (V == SEG ? 4 : 2);
+}
+
+template <typename T, int V, int SEG, int NV, int W>
+__global__ void __launch_bounds__(32 * row_warps<W>(), row_ctas_per_sm<V, SEG, NV>() * kRowWarps / row_warps<W>())
+group_norm_row_kernel(const T *__restrict__ x, const T *__restrict__ gamma, const T *__restrict__ beta,
+                      T *__restrict__ y, float *__restrict__ mean_out, float *__restrict__ rstd_out,
+                      GnShape sh, float eps, int act) {
+  extern __shared__ float row_smem[];
+  constexpr int P = pairs<V>();
+  __shared__ float red[W == 1 ? 1 : 4 * W];
+  const int me = W == 1 ? threadIdx.x & 31 : threadIdx.x;   // among the item's lanes
+  const int item = W == 1 ? threadIdx.x >> 5 : 0;           // among the CTA's items
+  const int64_t step = (int64_t)gridDim.x * (W == 1 ? kRowWarps : 1);
+  const int nv = (int)(sh.S * sh.L / V);
+  float *part = row_smem + item * row_smem_floats(sh);
+  float *gmean = part + nv, *grstd = gmean + sh.G;
+  const int Lv = sh.L / V, runv = sh.run / V;
+  const float n = (float)(sh.S * sh.run);
+  // a lane's vectors have the same channels in every item: gamma and beta stay in registers
+  float ga[NV][V / SEG], be[NV][V / SEG];
+  int grp[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int q = me + 32 * W * k;
+    const int c = q < nv ? q % Lv : 0;
+    grp[k] = c / runv;
+    load_affine<T, V, SEG>(gamma, c * V, sh.N, 1.0f, ga[k]);
+    load_affine<T, V, SEG>(beta, c * V, sh.N, 0.0f, be[k]);
+  }
+  for (int64_t b = (int64_t)blockIdx.x * (W == 1 ? kRowWarps : 1) + item; b < sh.B; b += step) {
+    const T *src = x + b * sh.S * sh.L + me * V;
+    Raw<T, V> raw[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (me + 32 * W * k < nv) raw[k] = load_raw<T, V>(src + 32 * W * k * V);
+    float m1 = 0.0f, r1 = 0.0f;   // G = 1
+    if (sh.G == 1) {
+      float2 s = both(0.0f), ss = both(0.0f);
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (me + 32 * W * k < nv) {
+          float2 v[P];
+          unpack(raw[k], v);
+#pragma unroll
+          for (int e = 0; e < P; ++e) s = add2(s, v[e]);
+        }
+      m1 = item_sum<W>(lanes_sum<V>(s), red) / n;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (me + 32 * W * k < nv) {
+          float2 v[P];
+          unpack(raw[k], v);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const float2 d = add2(v[e], both(-m1));
+            ss = fma2(d, d, ss);
+          }
+        }
+      r1 = rsqrtf(item_sum<W>(lanes_sum<V>(ss), red + W) / n + eps);
+      if (me == 0) {
+        if (mean_out) mean_out[b] = m1;
+        if (rstd_out) rstd_out[b] = r1;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (me + 32 * W * k < nv) {
+          float2 v[P], s = both(0.0f);
+          unpack(raw[k], v);
+#pragma unroll
+          for (int e = 0; e < P; ++e) s = add2(s, v[e]);
+          part[me + 32 * W * k] = lanes_sum<V>(s);
+        }
+      team_sync<W>();
+      group_sums<W>(part, gmean, sh, me);
+      team_sync<W>();
+      for (int g = me; g < sh.G; g += 32 * W) gmean[g] /= n;
+      team_sync<W>();
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (me + 32 * W * k < nv) {
+          const float2 m = both(-gmean[grp[k]]);
+          float2 v[P], s = both(0.0f);
+          unpack(raw[k], v);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const float2 d = add2(v[e], m);
+            s = fma2(d, d, s);
+          }
+          part[me + 32 * W * k] = lanes_sum<V>(s);
+        }
+      team_sync<W>();
+      group_sums<W>(part, grstd, sh, me);
+      team_sync<W>();
+      for (int g = me; g < sh.G; g += 32 * W) {
+        const float r = rsqrtf(grstd[g] / n + eps);
+        grstd[g] = r;
+        if (mean_out) mean_out[b * sh.G + g] = gmean[g];
+        if (rstd_out) rstd_out[b * sh.G + g] = r;
+      }
+      team_sync<W>();
+    }
+    T *dst = y + b * sh.S * sh.L + me * V;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (me + 32 * W * k >= nv) continue;
+      const float2 m = both(sh.G == 1 ? -m1 : -gmean[grp[k]]), r = both(sh.G == 1 ? r1 : grstd[grp[k]]);
+      float2 v[P];
+      unpack(raw[k], v);
+#pragma unroll
+      for (int e = 0; e < P; ++e)
+        v[e] = act_pair<T>(act, fma2(mul2(add2(v[e], m), r), affine_pair<V, SEG>(ga[k], e), affine_pair<V, SEG>(be[k], e)));
+      store_pairs<T, V>(dst + 32 * W * k * V, v);
+    }
+    if (sh.G > 1) team_sync<W>();   // the next item rewrites part, gmean and grstd
+  }
+}
+
+// Backward of the row form.  dgamma and dbeta: a lane keeps the sums of its
+// segments over its items; at the end the CTA's warps that share segments add
+// theirs in turn and the CTA writes one partial per field, part[cta][F][2].
+template <typename T, int V, int SEG, int NV, int W>
+__global__ void __launch_bounds__(32 * row_warps<W>(), row_backward_ctas_per_sm<V, SEG, NV>() * kRowWarps / row_warps<W>())
+group_norm_row_backward_kernel(const T *__restrict__ x, const T *__restrict__ dy, const float *__restrict__ mean,
+                               const float *__restrict__ rstd, const T *__restrict__ gamma,
+                               const T *__restrict__ beta, T *__restrict__ dx, float *__restrict__ part_out,
+                               GnShape sh, int act) {
+  extern __shared__ float row_smem[];
+  constexpr int NS = V / SEG, P = pairs<V>(), SP = seg_pairs<V, SEG>();
+  __shared__ float red[W == 1 ? 1 : 4 * W];
+  const int me = W == 1 ? threadIdx.x & 31 : threadIdx.x;   // among the item's lanes
+  const int item = W == 1 ? threadIdx.x >> 5 : 0;           // among the CTA's items
+  const int64_t step = (int64_t)gridDim.x * (W == 1 ? kRowWarps : 1);
+  const int nv = (int)(sh.S * sh.L / V);
+  float *part = row_smem + item * row_smem_floats(sh);
+  float *c1 = part + nv, *c2 = c1 + sh.G;
+  const int Lv = sh.L / V, runv = sh.run / V;
+  const float inv_n = 1.0f / (float)(sh.S * sh.run);
+  bool flip = false;
+  float ga[NV][NS], be[NV][NS];
+  float2 sg[NV][SP], sb[NV][SP];
+  int grp[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int q = me + 32 * W * k;
+    const int c = q < nv ? q % Lv : 0;
+    grp[k] = c / runv;
+    load_affine<T, V, SEG>(gamma, c * V, sh.N, 1.0f, ga[k]);
+    load_affine<T, V, SEG>(beta, c * V, sh.N, 0.0f, be[k]);
+#pragma unroll
+    for (int j = 0; j < SP; ++j) sg[k][j] = sb[k][j] = both(0.0f);
+  }
+  // xhat and gamma dz of pair e of vector k (dz too)
+  auto terms = [&](int k, const float2 &v, const float2 &d, float2 m, float2 r, int e, float2 &xh, float2 &dz) {
+    xh = mul2(add2(v, m), r);
+    dz = d;
+    if (act != EQLIN_ACT_NONE)
+      dz = mul2(dz, slope_pair<T>(act, fma2(xh, affine_pair<V, SEG>(ga[k], e), affine_pair<V, SEG>(be[k], e))));
+  };
+  for (int64_t b = (int64_t)blockIdx.x * (W == 1 ? kRowWarps : 1) + item; b < sh.B; b += step) {
+    const int64_t at = b * sh.S * sh.L + me * V;
+    Raw<T, V> rx[NV], rd[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (me + 32 * W * k < nv) {
+        rx[k] = load_raw<T, V>(x + at + 32 * W * k * V);
+        rd[k] = load_raw<T, V>(dy + at + 32 * W * k * V);
+      }
+    const float gm = sh.G == 1 ? __ldg(mean + b) : 0.0f, gr = sh.G == 1 ? __ldg(rstd + b) : 0.0f;
+    float s1 = 0.0f, s2 = 0.0f, p2[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int q = me + 32 * W * k;
+      p2[k] = 0.0f;
+      if (q >= nv) continue;
+      const float2 m = both(sh.G == 1 ? -gm : -__ldg(mean + b * sh.G + grp[k]));
+      const float2 r = both(sh.G == 1 ? gr : __ldg(rstd + b * sh.G + grp[k]));
+      float2 v[P], d[P], a1 = both(0.0f), a2 = both(0.0f);
+      unpack(rx[k], v);
+      unpack(rd[k], d);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        float2 xh, dz;
+        terms(k, v[e], d[e], m, r, e, xh, dz);
+        sb[k][seg_at<SEG>(e)] = add2(sb[k][seg_at<SEG>(e)], dz);
+        sg[k][seg_at<SEG>(e)] = fma2(dz, xh, sg[k][seg_at<SEG>(e)]);
+        const float2 dn = mul2(dz, affine_pair<V, SEG>(ga[k], e));
+        a1 = add2(a1, dn);
+        a2 = fma2(dn, xh, a2);
+      }
+      const float l1 = lanes_sum<V>(a1);
+      p2[k] = lanes_sum<V>(a2);
+      s1 += l1;
+      s2 += p2[k];
+      if (sh.G > 1) part[q] = l1;
+    }
+    if (sh.G == 1) {
+      item_sums<W>(s1, s2, red + (flip ? 2 * W : 0));
+      flip = !flip;
+      s1 *= inv_n;
+      s2 *= inv_n;
+    } else {
+      team_sync<W>();
+      group_sums<W>(part, c1, sh, me);
+      team_sync<W>();
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (me + 32 * W * k < nv) part[me + 32 * W * k] = p2[k];
+      team_sync<W>();
+      group_sums<W>(part, c2, sh, me);
+      team_sync<W>();
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int q = me + 32 * W * k;
+      if (q >= nv) continue;
+      const float2 m1 = both(sh.G == 1 ? -s1 : -c1[grp[k]] * inv_n), m2 = both(sh.G == 1 ? -s2 : -c2[grp[k]] * inv_n);
+      const float2 m = both(sh.G == 1 ? -gm : -__ldg(mean + b * sh.G + grp[k]));
+      const float2 r = both(sh.G == 1 ? gr : __ldg(rstd + b * sh.G + grp[k]));
+      float2 v[P], d[P];
+      unpack(rx[k], v);
+      unpack(rd[k], d);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        float2 xh, dz;
+        terms(k, v[e], d[e], m, r, e, xh, dz);
+        v[e] = mul2(r, fma2(xh, m2, fma2(dz, affine_pair<V, SEG>(ga[k], e), m1)));
+      }
+      store_pairs<T, V>(dx + at + 32 * W * k * V, v);
+    }
+    if (sh.G > 1) team_sync<W>();
+  }
+  if (!part_out) return;   // the same for the whole grid
+  // segment sums of the CTA: seg[(q NS + j)], q over the item's vectors
+  __syncthreads();
+  float *seg_b = row_smem, *seg_g = row_smem + nv * NS;
+  constexpr int kItems = W == 1 ? kRowWarps : 1;
+  for (int w = 0; w < kItems; ++w) {
+    if (item == w) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int q = me + 32 * W * k;
+        if (q >= nv) continue;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const float vb = seg_value<V, SEG>(sb[k], j), vg = seg_value<V, SEG>(sg[k], j);
+          seg_b[q * NS + j] = w == 0 ? vb : seg_b[q * NS + j] + vb;
+          seg_g[q * NS + j] = w == 0 ? vg : seg_g[q * NS + j] + vg;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const int per_field = sh.N / SEG, per_pos = sh.L / SEG;
+  for (int f = threadIdx.x; f < sh.F; f += blockDim.x) {
+    float a = 0.0f, c = 0.0f;
+    for (int s = 0; s < (int)sh.S; ++s)
+      for (int j = 0; j < per_field; ++j) {
+        a += seg_b[s * per_pos + f * per_field + j];
+        c += seg_g[s * per_pos + f * per_field + j];
+      }
+    float *dst = part_out + ((int64_t)blockIdx.x * sh.F + f) * 2;
+    dst[0] = a;
+    dst[1] = c;
+  }
+}
+
+// ------------------------------------------------------------ chunk kernels
+
+// Running statistics of n values.
+struct Stats {
+  float n, mean, m2;
+};
+// Chan, Golub and LeVeque (1979), pairwise update.
+__device__ __forceinline__ Stats join(const Stats &a, const Stats &b) {
+  Stats r;
+  r.n = a.n + b.n;
+  if (r.n == 0.0f) return a;
+  const float d = b.mean - a.mean, w = __fdividef(b.n, r.n);
+  r.mean = fmaf(d, w, a.mean);
+  r.m2 = a.m2 + fmaf(d * d * a.n, w, b.m2);
+  return r;
+}
+// Over the lanes of aligned teams of `team` lanes (a power of two); the result is
+// the team's first lane's.
+__device__ __forceinline__ Stats team_join(Stats a, int team) {
+  for (int o = 1; o < team; o <<= 1) {
+    Stats b;
+    b.n = __shfl_down_sync(0xffffffffu, a.n, o, team);
+    b.mean = __shfl_down_sync(0xffffffffu, a.mean, o, team);
+    b.m2 = __shfl_down_sync(0xffffffffu, a.m2, o, team);
+    a = join(a, b);
+  }
+  return a;
+}
+__device__ __forceinline__ float team_sum(float a, int team) {
+  for (int o = 1; o < team; o <<= 1) a += __shfl_down_sync(0xffffffffu, a, o, team);
+  return a;
+}
+// Lanes per group when a CTA of `threads` joins something for `groups` groups: as
+// many as make one round of it, 1 to 32.
+__device__ __forceinline__ int team_lanes(int groups, int threads) {
+  int t = 32;
+  while (t > 1 && t * groups > threads) t >>= 1;
+  return t;
+}
+
+constexpr int kAtOnce = 4;   // positions a thread reads together
+
+// Statistics of U vectors `next` values apart, two-pass.
+template <typename T, int V, int U>
+__device__ __forceinline__ Stats block_stats(const T *src, int64_t next) {
+  constexpr int P = pairs<V>();
+  Raw<T, V> raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) raw[u] = load_raw<T, V>(src + u * next);
+  float2 v[U][P], sum = both(0.0f), ss = both(0.0f);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    unpack(raw[u], v[u]);
+#pragma unroll
+    for (int e = 0; e < P; ++e) sum = add2(sum, v[u][e]);
+  }
+  Stats blk;
+  blk.n = (float)(U * V);
+  blk.mean = lanes_sum<V>(sum) * (1.0f / (U * V));   // U V is a power of two
+  const float2 m = both(-blk.mean);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const float2 d = add2(v[u][e], m);
+      ss = fma2(d, d, ss);
+    }
+  blk.m2 = lanes_sum<V>(ss);
+  return blk;
+}
+
+// part[(b chunks + chunk) G + g] = statistics of the chunk's values of group g.
+template <typename T, int V>
+__global__ void __launch_bounds__(kColThreads, 2)
+group_norm_stats_kernel(const T *__restrict__ x, float4 *__restrict__ part, GnShape sh) {
+  extern __shared__ float col_smem[];
+  const int64_t b = blockIdx.x / sh.chunks;
+  const int chunk = (int)(blockIdx.x - b * sh.chunks);
+  const Tiling tl = col_tiling(sh);
+  Stats *ts = reinterpret_cast<Stats *>(col_smem);   // [threads]
+  Stats *gs = ts + tl.threads;                       // [G]
+  const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
+  const int tid = threadIdx.x;
+  const int Lv = sh.L / V, runv = sh.run / V;
+  const int pl = tid / tl.tile, col0 = tid % tl.tile;
+  for (int g = tid; g < sh.G; g += blockDim.x) gs[g] = Stats{0.0f, 0.0f, 0.0f};
+  for (int t = 0; t < tl.tiles; ++t) {
+    const int col = t * tl.tile + col0;
+    Stats st{0.0f, 0.0f, 0.0f};
+    if (pl < tl.lanes && col < Lv) {
+      const T *src = x + (b * sh.S + s0 + pl) * sh.L + (int64_t)col * V;
+      const int64_t next = (int64_t)tl.lanes * sh.L;   // to the thread's next position
+      int left = (int)((s1 - s0 - pl + tl.lanes - 1) / tl.lanes);
+      for (; left >= kAtOnce; left -= kAtOnce, src += kAtOnce * next) st = join(st, block_stats<T, V, kAtOnce>(src, next));
+      for (; left > 0; --left, src += next) st = join(st, block_stats<T, V, 1>(src, next));
+    }
+    ts[tid] = st;
+    __syncthreads();
+    // a team of lanes per group joins the tile's columns of the group, all position lanes
+    const int first = t * tl.tile, last = first + tl.tile < Lv ? first + tl.tile : Lv;
+    const int g_first = first / runv, groups = (last - 1) / runv - g_first + 1;
+    const int team = team_lanes(groups, blockDim.x), member = tid & (team - 1);
+    for (int k0 = 0; k0 < groups; k0 += blockDim.x / team) {
+      const int k = k0 + tid / team, g = g_first + k;
+      Stats acc{0.0f, 0.0f, 0.0f};
+      if (k < groups) {
+        const int a = g * runv > first ? g * runv : first;
+        const int z = (g + 1) * runv < last ? (g + 1) * runv : last;
+        const int w = z - a;
+        for (int l = 0; l < tl.lanes; ++l)
+          for (int j = member; j < w; j += team) acc = join(acc, ts[l * tl.tile + a - first + j]);
+      }
+      acc = team_join(acc, team);
+      if (k < groups && member == 0) gs[g] = join(gs[g], acc);
+    }
+    __syncthreads();
+  }
+  for (int g = tid; g < sh.G; g += blockDim.x)
+    part[(b * sh.chunks + chunk) * sh.G + g] = make_float4(gs[g].n, gs[g].mean, gs[g].m2, 0.0f);
+}
+
+template <typename T, int V, int SEG>
+__global__ void __launch_bounds__(kColThreads, 2)
+group_norm_apply_kernel(const T *__restrict__ x, const T *__restrict__ gamma, const T *__restrict__ beta,
+                        const float4 *__restrict__ part, T *__restrict__ y, float *__restrict__ mean_out,
+                        float *__restrict__ rstd_out, GnShape sh, float eps, int act) {
+  extern __shared__ float col_smem[];
+  constexpr int P = pairs<V>();
+  const int64_t unit = (int64_t)gridDim.x - 1 - blockIdx.x;
+  const int64_t b = unit / sh.chunks;
+  const int chunk = (int)(unit - b * sh.chunks);
+  float2 *gs = reinterpret_cast<float2 *>(col_smem);   // [G] mean, rstd
+  const Tiling tl = col_tiling(sh);
+  const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
+  const int tid = threadIdx.x;
+  const int team = team_lanes(sh.G, blockDim.x), member = tid & (team - 1);
+  for (int g0 = 0; g0 < sh.G; g0 += blockDim.x / team) {
+    const int g = g0 + tid / team;
+    Stats acc{0.0f, 0.0f, 0.0f};
+    if (g < sh.G)
+      for (int c = member; c < sh.chunks; c += team) {
+        const float4 p = part[(b * sh.chunks + c) * sh.G + g];
+        acc = join(acc, Stats{p.x, p.y, p.z});
+      }
+    acc = team_join(acc, team);
+    if (g < sh.G && member == 0) {
+      const float r = rsqrtf(acc.m2 / acc.n + eps);
+      gs[g] = make_float2(acc.mean, r);
+      if (chunk == 0) {
+        if (mean_out) mean_out[b * sh.G + g] = acc.mean;
+        if (rstd_out) rstd_out[b * sh.G + g] = r;
+      }
+    }
+  }
+  __syncthreads();
+  const int Lv = sh.L / V, runv = sh.run / V;
+  const int pl = tid / tl.tile;
+  if (pl >= tl.lanes) return;
+  for (int col = tid % tl.tile; col < Lv; col += tl.tile) {
+    const float2 m = both(-gs[col / runv].x);
+    float ga[V / SEG], be[V / SEG];
+    load_affine<T, V, SEG>(gamma, col * V, sh.N, 1.0f, ga);
+    load_affine<T, V, SEG>(beta, col * V, sh.N, 0.0f, be);
+#pragma unroll
+    for (int k = 0; k < V / SEG; ++k) ga[k] *= gs[col / runv].y;
+    auto value = [&](const Raw<T, V> &raw, T *dst) {
+      float2 v[P];
+      unpack(raw, v);
+#pragma unroll
+      for (int e = 0; e < P; ++e)
+        v[e] = act_pair<T>(act, fma2(add2(v[e], m), affine_pair<V, SEG>(ga, e), affine_pair<V, SEG>(be, e)));
+      store_pairs<T, V>(dst, v);
+    };
+    const int64_t off = (b * sh.S + s0 + pl) * sh.L + (int64_t)col * V, next = (int64_t)tl.lanes * sh.L;
+    const T *src = x + off;
+    T *dst = y + off;
+    int left = (int)((s1 - s0 - pl + tl.lanes - 1) / tl.lanes);
+    for (; left >= kAtOnce; left -= kAtOnce, src += kAtOnce * next, dst += kAtOnce * next) {
+      Raw<T, V> raw[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) raw[u] = load_last<T, V>(src + u * next);
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) value(raw[u], dst + u * next);
+    }
+    for (; left > 0; --left, src += next, dst += next) value(load_last<T, V>(src), dst);
+  }
+}
+
+// Backward, first pass of a chunk: part_f[(b chunks + chunk) F + f] = (sum dz,
+// sum dz xhat), and per group part_g[(b chunks + chunk) G + g] = the same sums
+// weighted with gamma.
+template <typename T, int V, int SEG>
+__global__ void __launch_bounds__(kColThreads, 2)
+group_norm_backward_sums_kernel(const T *__restrict__ x, const T *__restrict__ dy, const float *__restrict__ mean,
+                                const float *__restrict__ rstd, const T *__restrict__ gamma,
+                                const T *__restrict__ beta, float2 *part_f, float2 *__restrict__ part_g, GnShape sh,
+                                int act) {
+  extern __shared__ float col_smem[];
+  constexpr int NS = V / SEG, P = pairs<V>(), SP = seg_pairs<V, SEG>();
+  constexpr int kTwo = 2;
+  const int64_t b = blockIdx.x / sh.chunks;
+  const int chunk = (int)(blockIdx.x - b * sh.chunks);
+  float2 *seg = reinterpret_cast<float2 *>(col_smem);   // [lanes][tile NS]
+  const Tiling tl = col_tiling(sh);
+  const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
+  const int tid = threadIdx.x;
+  const int Lv = sh.L / V, runv = sh.run / V;
+  const int pl = tid / tl.tile, col0 = tid % tl.tile;
+  float2 *out_f = part_f + (b * sh.chunks + chunk) * sh.F;
+  for (int t = 0; t < tl.tiles; ++t) {
+    const int col = t * tl.tile + col0;
+    float2 sb[SP], sg[SP];
+#pragma unroll
+    for (int j = 0; j < SP; ++j) sb[j] = sg[j] = both(0.0f);
+    if (pl < tl.lanes && col < Lv) {
+      const float2 m = both(-__ldg(mean + b * sh.G + col / runv)), r = both(__ldg(rstd + b * sh.G + col / runv));
+      float ga[NS], be[NS];
+      load_affine<T, V, SEG>(gamma, col * V, sh.N, 1.0f, ga);
+      load_affine<T, V, SEG>(beta, col * V, sh.N, 0.0f, be);
+      auto add = [&](const Raw<T, V> &rx, const Raw<T, V> &rd) {
+        float2 v[P], d[P];
+        unpack(rx, v);
+        unpack(rd, d);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const float2 xh = mul2(add2(v[e], m), r);
+          float2 dz = d[e];
+          if (act != EQLIN_ACT_NONE)
+            dz = mul2(dz, slope_pair<T>(act, fma2(xh, affine_pair<V, SEG>(ga, e), affine_pair<V, SEG>(be, e))));
+          sb[seg_at<SEG>(e)] = add2(sb[seg_at<SEG>(e)], dz);
+          sg[seg_at<SEG>(e)] = fma2(dz, xh, sg[seg_at<SEG>(e)]);
+        }
+      };
+      const int64_t off = (b * sh.S + s0 + pl) * sh.L + (int64_t)col * V, next = (int64_t)tl.lanes * sh.L;
+      const T *px = x + off, *pd = dy + off;
+      int left = (int)((s1 - s0 - pl + tl.lanes - 1) / tl.lanes);
+      for (; left >= kTwo; left -= kTwo, px += kTwo * next, pd += kTwo * next) {
+        Raw<T, V> rx[kTwo], rd[kTwo];
+#pragma unroll
+        for (int u = 0; u < kTwo; ++u) {
+          rx[u] = load_raw<T, V>(px + u * next);
+          rd[u] = load_raw<T, V>(pd + u * next);
+        }
+#pragma unroll
+        for (int u = 0; u < kTwo; ++u) add(rx[u], rd[u]);
+      }
+      for (; left > 0; --left, px += next, pd += next) add(load_raw<T, V>(px), load_raw<T, V>(pd));
+    }
+    if (pl < tl.lanes)
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+        seg[(pl * tl.tile + col0) * NS + j] = make_float2(seg_value<V, SEG>(sb, j), seg_value<V, SEG>(sg, j));
+    __syncthreads();
+    // one thread per field of the tile: its segments, all position lanes
+    const int per_field = sh.N / SEG;
+    const int first = t * tl.tile, last = first + tl.tile < Lv ? first + tl.tile : Lv;
+    const int f0 = (int)((int64_t)first * V / sh.N), nf = (int)((int64_t)(last - first) * V / sh.N);
+    for (int f = tid; f < nf; f += blockDim.x) {
+      float a = 0.0f, c = 0.0f;
+      for (int l = 0; l < tl.lanes; ++l)
+        for (int j = 0; j < per_field; ++j) {
+          const float2 p = seg[l * tl.tile * NS + f * per_field + j];
+          a += p.x;
+          c += p.y;
+        }
+      out_f[f0 + f] = make_float2(a, c);
+    }
+    __syncthreads();   // the CTA's own global writes are then visible to its threads
+  }
+  const int fpg = sh.F / sh.G;
+  const int team = team_lanes(sh.G, blockDim.x), member = tid & (team - 1);
+  for (int g0 = 0; g0 < sh.G; g0 += blockDim.x / team) {
+    const int g = g0 + tid / team;
+    float a = 0.0f, q = 0.0f;
+    if (g < sh.G)
+      for (int j = member; j < fpg; j += team) {
+        const float2 p = out_f[g * fpg + j];
+        const float w = gamma ? to_f32(__ldg(gamma + g * fpg + j)) : 1.0f;
+        a = fmaf(w, p.x, a);
+        q = fmaf(w, p.y, q);
+      }
+    a = team_sum(a, team);
+    q = team_sum(q, team);
+    if (g < sh.G && member == 0) part_g[(b * sh.chunks + chunk) * sh.G + g] = make_float2(a, q);
+  }
+}
+
+// Second pass: dx.
+template <typename T, int V, int SEG>
+__global__ void __launch_bounds__(kColThreads, 2)
+group_norm_backward_apply_kernel(const T *__restrict__ x, const T *__restrict__ dy, const float *__restrict__ mean,
+                                 const float *__restrict__ rstd, const T *__restrict__ gamma,
+                                 const T *__restrict__ beta, const float2 *__restrict__ part_g, T *__restrict__ dx,
+                                 GnShape sh, int act) {
+  extern __shared__ float col_smem[];
+  constexpr int P = pairs<V>();
+  constexpr int kTwo = 2;
+  const int64_t unit = (int64_t)gridDim.x - 1 - blockIdx.x;
+  const int64_t b = unit / sh.chunks;
+  const int chunk = (int)(unit - b * sh.chunks);
+  float2 *cs = reinterpret_cast<float2 *>(col_smem);   // [G] the group's two means
+  const Tiling tl = col_tiling(sh);
+  const int64_t s0 = chunk * sh.per, s1 = s0 + sh.per < sh.S ? s0 + sh.per : sh.S;
+  const int tid = threadIdx.x;
+  const float inv_n = 1.0f / ((float)sh.S * (float)sh.run);
+  const int team = team_lanes(sh.G, blockDim.x), member = tid & (team - 1);
+  for (int g0 = 0; g0 < sh.G; g0 += blockDim.x / team) {
+    const int g = g0 + tid / team;
+    float a = 0.0f, q = 0.0f;
+    if (g < sh.G)
+      for (int c = member; c < sh.chunks; c += team) {
+        const float2 p = part_g[(b * sh.chunks + c) * sh.G + g];
+        a += p.x;
+        q += p.y;
+      }
+    a = team_sum(a, team);
+    q = team_sum(q, team);
+    if (g < sh.G && member == 0) cs[g] = make_float2(-a * inv_n, -q * inv_n);
+  }
+  __syncthreads();
+  const int Lv = sh.L / V, runv = sh.run / V;
+  const int pl = tid / tl.tile;
+  if (pl >= tl.lanes) return;
+  for (int col = tid % tl.tile; col < Lv; col += tl.tile) {
+    const int g = col / runv;
+    const float2 m = both(-__ldg(mean + b * sh.G + g)), r = both(__ldg(rstd + b * sh.G + g));
+    const float2 m1 = both(cs[g].x), m2 = both(cs[g].y);
+    float ga[V / SEG], be[V / SEG];
+    load_affine<T, V, SEG>(gamma, col * V, sh.N, 1.0f, ga);
+    load_affine<T, V, SEG>(beta, col * V, sh.N, 0.0f, be);
+    auto value = [&](const Raw<T, V> &rx, const Raw<T, V> &rd, T *dst) {
+      float2 v[P], d[P];
+      unpack(rx, v);
+      unpack(rd, d);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const float2 xh = mul2(add2(v[e], m), r);
+        float2 dz = d[e];
+        if (act != EQLIN_ACT_NONE)
+          dz = mul2(dz, slope_pair<T>(act, fma2(xh, affine_pair<V, SEG>(ga, e), affine_pair<V, SEG>(be, e))));
+        v[e] = mul2(r, fma2(xh, m2, fma2(dz, affine_pair<V, SEG>(ga, e), m1)));
+      }
+      store_pairs<T, V>(dst, v);
+    };
+    const int64_t off = (b * sh.S + s0 + pl) * sh.L + (int64_t)col * V, next = (int64_t)tl.lanes * sh.L;
+    const T *px = x + off, *pd = dy + off;
+    T *dst = dx + off;
+    int left = (int)((s1 - s0 - pl + tl.lanes - 1) / tl.lanes);
+    for (; left >= kTwo; left -= kTwo, px += kTwo * next, pd += kTwo * next, dst += kTwo * next) {
+      Raw<T, V> rx[kTwo], rd[kTwo];
+#pragma unroll
+      for (int u = 0; u < kTwo; ++u) {
+        rx[u] = load_last<T, V>(px + u * next);
+        rd[u] = load_last<T, V>(pd + u * next);
+      }
+#pragma unroll
+      for (int u = 0; u < kTwo; ++u) value(rx[u], rd[u], dst + u * next);
+    }
+    for (; left > 0; --left, px += next, pd += next, dst += next) value(load_last<T, V>(px), load_last<T, V>(pd), dst);
+  }
+}
+
+// dgamma, dbeta from R partials [R][F] of (sum dz, sum dz xhat): 16 fields per
+// CTA, 64 threads per field, each a fixed share of the partials.
+template <typename T>
+__global__ void __launch_bounds__(1024)
+group_norm_affine_grad_kernel(const float2 *__restrict__ part, int64_t R, int F, T *__restrict__ dgamma,
+                              T *__restrict__ dbeta) {
+  __shared__ float2 acc[64][17];
+  const int fl = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int f = blockIdx.x * 16 + fl;
+  float a = 0.0f, q = 0.0f;
+  if (f < F) {
+#pragma unroll 8
+    for (int64_t p = r; p < R; p += 64) {
+      const float2 v = __ldg(part + p * F + f);
+      a += v.x;
+      q += v.y;
+    }
+  }
+  acc[r][fl] = make_float2(a, q);
+  __syncthreads();
+  // warp w < 16 joins field w
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (w < 16) {
+    const float2 u = acc[lane][w], v = acc[lane + 32][w];
+    a = warp_sum(u.x + v.x);
+    q = warp_sum(u.y + v.y);
+    if (lane == 0 && blockIdx.x * 16 + w < F) {
+      if (dbeta) dbeta[blockIdx.x * 16 + w] = from_f32<T>(a);
+      if (dgamma) dgamma[blockIdx.x * 16 + w] = from_f32<T>(q);
+    }
+  }
+}
+
+// ------------------------------------------------------------ launches
+
+template <typename T, int V, int SEG, int NV, int W>
+int row_forward(const NormTensors &t, const GnShape &sh, float eps, int act, cudaStream_t s) {
+  const size_t smem = (size_t)(W == 1 ? kRowWarps : 1) * row_smem_floats(sh) * sizeof(float);
+  const int64_t most = 148 * row_ctas_per_sm<V, SEG, NV>() * kRowWarps / row_warps<W>();
+  group_norm_row_kernel<T, V, SEG, NV, W><<<(unsigned)row_ctas(sh, most), 32 * row_warps<W>(), smem, s>>>(
+      (const T *)t.x, (const T *)t.gamma, (const T *)t.beta, (T *)t.y, t.mean_out, t.rstd_out, sh, eps, act);
+  return check_launch("group norm (rows)");
+}
+
+template <typename T, int V, int SEG, int NV, int W>
+int row_backward(const NormTensors &t, const GnShape &sh, int act, float *part, int64_t *ctas, cudaStream_t s) {
+  size_t floats = (size_t)(W == 1 ? kRowWarps : 1) * row_smem_floats(sh);
+  const size_t segs = 2 * (size_t)(sh.S * sh.L / SEG);
+  if (part && segs > floats) floats = segs;
+  constexpr int64_t most = 148 * row_backward_ctas_per_sm<V, SEG, NV>() * kRowWarps / row_warps<W>();
+  static_assert(most <= kRowCtas, "the partials' workspace");
+  *ctas = row_ctas(sh, most);
+  group_norm_row_backward_kernel<T, V, SEG, NV, W><<<(unsigned)*ctas, 32 * row_warps<W>(), floats * sizeof(float), s>>>(
+      (const T *)t.x, (const T *)t.dy, t.mean, t.rstd, (const T *)t.gamma, (const T *)t.beta, (T *)t.y, part, sh, act);
+  return check_launch("group norm backward (rows)");
+}
+
+template <typename T, int V, int SEG>
+int forward_v(const NormTensors &t, const GnShape &sh, float eps, int act, void *ws, cudaStream_t s) {
+  if (row_form(sh)) {
+    const int nv = (int)(sh.S * sh.L / V), warps = row_warps_for(sh);
+    if (nv <= 32) return row_forward<T, V, SEG, 1, 1>(t, sh, eps, act, s);
+    if (nv <= 96) return row_forward<T, V, SEG, 3, 1>(t, sh, eps, act, s);
+    if (warps == 1) return row_forward<T, V, SEG, kRowVecs, 1>(t, sh, eps, act, s);
+    if constexpr (V * sizeof(T) >= 8) {
+      if (warps == 2) return row_forward<T, V, SEG, kRowVecs, 2>(t, sh, eps, act, s);
+      if (warps == 4) return row_forward<T, V, SEG, kRowVecs, 4>(t, sh, eps, act, s);
+      if (warps == 8) return row_forward<T, V, SEG, kRowVecs, 8>(t, sh, eps, act, s);
+      if constexpr (V == SEG) return row_forward<T, V, SEG, kRowVecs, 16>(t, sh, eps, act, s);
+    }
+  }
+  const Tiling tl = col_tiling(sh);
+  const unsigned grid = (unsigned)(sh.B * sh.chunks);
+  float4 *part = static_cast<float4 *>(ws);
+  group_norm_stats_kernel<T, V><<<grid, tl.threads, (tl.threads + sh.G) * sizeof(Stats), s>>>((const T *)t.x, part, sh);
+  const int rc = check_launch("group norm (statistics)");
+  if (rc) return rc;
+  group_norm_apply_kernel<T, V, SEG><<<grid, tl.threads, sh.G * sizeof(float2), s>>>(
+      (const T *)t.x, (const T *)t.gamma, (const T *)t.beta, part, (T *)t.y, t.mean_out, t.rstd_out, sh, eps, act);
+  return check_launch("group norm");
+}
+
+template <typename T>
+int affine_grad(const NormTensors &t, const float2 *part, int64_t P, int F, cudaStream_t s) {
+  if (!t.dgamma && !t.dbeta) return EQLIN_OK;
+  group_norm_affine_grad_kernel<T><<<(unsigned)((F + 15) / 16), 1024, 0, s>>>(part, P, F, (T *)t.dgamma, (T *)t.dbeta);
+  return check_launch("group norm backward (dgamma, dbeta)");
+}
+
+template <typename T, int V, int SEG>
+int backward_v(const NormTensors &t, const GnShape &sh, int act, void *ws, cudaStream_t s) {
+  char *w = static_cast<char *>(ws);
+  int rc;
+  if (row_form(sh)) {
+    const int nv = (int)(sh.S * sh.L / V), warps = row_warps_for(sh);
+    float *part = t.dgamma || t.dbeta ? reinterpret_cast<float *>(w) : nullptr;
+    int64_t ctas = 0;
+    rc = nv <= 32   ? row_backward<T, V, SEG, 1, 1>(t, sh, act, part, &ctas, s)
+         : nv <= 96 ? row_backward<T, V, SEG, 3, 1>(t, sh, act, part, &ctas, s)
+                    : EQLIN_OK;
+    if (nv > 96 && warps == 1) rc = row_backward<T, V, SEG, kRowVecs, 1>(t, sh, act, part, &ctas, s);
+    if constexpr (V * sizeof(T) >= 8) {
+      if (warps == 2) rc = row_backward<T, V, SEG, kRowVecs, 2>(t, sh, act, part, &ctas, s);
+      if (warps == 4) rc = row_backward<T, V, SEG, kRowVecs, 4>(t, sh, act, part, &ctas, s);
+      if (warps == 8) rc = row_backward<T, V, SEG, kRowVecs, 8>(t, sh, act, part, &ctas, s);
+      if constexpr (V == SEG) {
+        if (warps == 16) rc = row_backward<T, V, SEG, kRowVecs, 16>(t, sh, act, part, &ctas, s);
+      }
+    }
+    if (rc) return rc;
+    return affine_grad<T>(t, reinterpret_cast<const float2 *>(w), ctas, sh.F, s);
+  }
+  const BackwardParts p = backward_parts(sh);
+  const Tiling tl = col_tiling(sh);
+  float2 *part_f = reinterpret_cast<float2 *>(w + p.field), *part_g = reinterpret_cast<float2 *>(w + p.group);
+  const unsigned grid = (unsigned)(sh.B * sh.chunks);
+  group_norm_backward_sums_kernel<T, V, SEG>
+      <<<grid, tl.threads, (size_t)tl.lanes * tl.tile * (V / SEG) * sizeof(float2), s>>>(
+          (const T *)t.x, (const T *)t.dy, t.mean, t.rstd, (const T *)t.gamma, (const T *)t.beta, part_f, part_g, sh, act);
+  if ((rc = check_launch("group norm backward (sums)"))) return rc;
+  group_norm_backward_apply_kernel<T, V, SEG><<<grid, tl.threads, sh.G * sizeof(float2), s>>>(
+      (const T *)t.x, (const T *)t.dy, t.mean, t.rstd, (const T *)t.gamma, (const T *)t.beta, part_g, (T *)t.y, sh, act);
+  if ((rc = check_launch("group norm backward"))) return rc;
+  return affine_grad<T>(t, part_f, sh.B * sh.chunks, sh.F, s);
+}
+
+// SEG = gcd(N, V): values that share a field.
+template <typename T, int V, int SEG>
+int dispatch_seg(bool backward, const NormTensors &t, const GnShape &sh, float eps, int act, void *ws, cudaStream_t s) {
+  if constexpr (SEG > 1) {
+    if (sh.N % SEG != 0) return dispatch_seg<T, V, SEG / 2>(backward, t, sh, eps, act, ws, s);
+  }
+  return backward ? backward_v<T, V, SEG>(t, sh, act, ws, s) : forward_v<T, V, SEG>(t, sh, eps, act, ws, s);
+}
+
+template <typename T>
+int dispatch_vec(bool backward, const NormTensors &t, const GnShape &sh, float eps, int act, void *ws, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (sh.vec == 8) return dispatch_seg<T, 8, 8>(backward, t, sh, eps, act, ws, s);
+  }
+  if (sh.vec == 4) return dispatch_seg<T, 4, 4>(backward, t, sh, eps, act, ws, s);
+  if (sh.vec == 2) return dispatch_seg<T, 2, 2>(backward, t, sh, eps, act, ws, s);
+  return dispatch_seg<T, 1, 1>(backward, t, sh, eps, act, ws, s);
+}
+
+}  // namespace
+
+// T is fixed by the including unit, so that the three types build side by side.
+template <>
+int launch_group_norm_t<EQLIN_NORM_TYPE>(bool backward, const NormTensors &t, const GnShape &sh, float eps, int act,
+                                         void *ws, cudaStream_t s) {
+  return dispatch_vec<EQLIN_NORM_TYPE>(backward, t, sh, eps, act, ws, s);
+}
+
+}  // namespace eqlin

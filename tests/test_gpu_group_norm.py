@@ -122,6 +122,38 @@ def test_rows(shape, G, dtype):
         check(x, G, gamma, beta, 1e-5, act, dy)
 
 
+# items of 2 to 16 warps (wide tokens, small maps): each count of warps at its ends, fields that share a vector, more
+# items than run at once, and the first sizes past the widest
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape,G", [
+    ((7, 161, 8), 1), ((5, 320, 8), 32), ((3001, 321, 8), 1), ((4, 640, 8), 4), ((650, 641, 8), 1), ((3, 1280, 8), 5),
+    ((2, 1281, 8), 1), ((301, 10, 160, 8), 8), ((2, 2560, 8), 2560 // 8), ((2, 2561, 8), 1), ((9, 3, 96, 12), 8),
+    ((33, 4, 80, 6), 1), ((5, 7, 80, 6), 20), ((6, 2, 1000, 3), 1), ((5, 1, 1500, 4), 1), ((4, 768, 8), 768),
+    ((3, 1900, 3), 1), ((3, 2000, 2), 500),
+    ((3, 6000, 1), 1), ((3, 6008, 1), 1), ((5, 2000, 3), 1), ((3, 2008, 3), 1), ((2, 768, 8), 2), ((2, 1200, 16), 3),
+])
+def test_items_of_several_warps(shape, G, dtype):
+    x, gamma, beta, dy = tensors(shape, dtype, 14)
+    for act in ("none", "silu", "gelu"):
+        check(x, G, gamma, beta, 1e-5, act, dy)
+
+
+def test_items_of_several_warps_repeat_and_stay_in_bounds():
+    for shape, G in [((2500, 400, 8), 1), ((1500, 400, 8), 16), ((400, 9, 100, 8), 4), ((40, 2500, 8), 1)]:
+        x, gamma, beta, dy = tensors(shape, torch.bfloat16, 15)
+        n = x.numel()
+        guard = torch.full((n + 512,), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = guard[256:256 + n].view(shape)
+        first = [t.clone() for t in eq.group_norm(x, G, gamma, beta, y=y)]
+        grads = [t.clone() for t in eq.group_norm_backward(x, dy, first[1], first[2], G, gamma, beta, dx=y)]
+        for _ in range(3):
+            for a, b in zip(eq.group_norm(x, G, gamma, beta, y=y), first):
+                assert torch.equal(a, b)
+            for a, b in zip(eq.group_norm_backward(x, dy, first[1], first[2], G, gamma, beta, dx=y), grads):
+                assert torch.equal(a, b)
+        assert (guard[:256] == 7).all() and (guard[256 + n:] == 7).all()
+
+
 # maps in chunks: ragged positions, odd groups and slots, positions wider than a CTA, one position only
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("shape,G", [
