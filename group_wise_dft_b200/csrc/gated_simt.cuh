@@ -15,6 +15,9 @@
 //  - few tokens: with a handful of tokens the weights are what is read and
 //    only a wide split hides their latency: a CTA takes 8 outputs and splits
 //    the input fields 32 ways over its threads, joined in a fixed order.
+// Measured: one token, 160 -> 432, C_8, 4.4 MB of weight spectra in about 5 us, a wave
+// of latency; 1001 tokens, 37 -> 101, C_6, fp32 15 us of small tiles, bound by their
+// shared-memory reads (6 FMAs for a broadcast word and a weight word).
 #pragma once
 
 #include "activations.cuh"

@@ -589,7 +589,9 @@ __device__ __forceinline__ void d8_epilogue_group(uint32_t tb, int fg, int half,
 // is how the data and weight gradients read them: S[c][token][field].  A thread's
 // pair is 4 bytes of each coordinate's row; the four lanes of a quad exchange theirs
 // so that each lane has 16 bytes of two coordinates per group, 32 with the next
-// group's: whole sectors (4-byte stores took 694 us, at 160 -> 432, T = 65536).
+// group's: whole sectors (4-byte stores took 694 us, at 160 -> 432, T = 65536; so 635).
+// h of T = 131072 takes 590 us, 522 of them without any epilogue: the products are
+// paced by the x transforms and the weight ring, the epilogue by the issue slots left.
 // The activations are the paired forms of tc_transforms.cuh: good to well below the
 // operand rounding of the products.  Not inlined, as neg16_epilogue_group.
 template <bool H>
